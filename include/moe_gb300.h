@@ -40,6 +40,8 @@
  *     word at the start of the workspace and read back with
  *     moe_get_device_status or moe_read_device_status.
  *   - Calls that share a workspace must not overlap on the GPU.
+ *   - The training-step operators (layer norm, router losses, gradient norm,
+ *     AdamW) take other element types, row strides and any d: see each.
  *   - Supported sizes: 1 <= E <= 1024, 1 <= k <= min(E, 32), 0 <= T,
  *     T*k < 2^31.  The GEMM stages and moe_forward need d and f to be
  *     multiples of 64 in [64, 65536] (whole 128-byte K blocks for the
@@ -585,6 +587,173 @@ MOE_API moe_status_t moe_forward_host_stream(const void* const* x_host, const fl
                                      int32_t renormalize, void* workspace,
                                      size_t workspace_bytes, moe_stream_t stream,
                                      moe_stream_t copy_in, moe_stream_t copy_out);
+
+/* ------------------------------------------------------------------------
+ * The training step around the layer: the norm before it, the auxiliary
+ * losses of its router, the norm of its gradients and the AdamW step over
+ * them.  None of the four waits for the GPU or needs a status word; each
+ * gives the same bits for the same inputs on every call.
+ * ---------------------------------------------------------------------- */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype_t;
+
+/* ------------------------------------------------------------------------
+ * Layer norm of the rows of x [T, d], of x + residual when a residual is
+ * given (the residual stream before a pre-norm layer):
+ *   z = round(x + residual)       the new residual stream, in the rows' type
+ *   mu = mean_j z,  r = 1 / sqrt(mean_j (z - mu)^2 + eps)
+ *   y = round((z - mu) * r * weight + bias)
+ *   x, residual  rows of `dtype`, unit stride along d, *_stride elements
+ *                between rows; residual optional;
+ *   weight, bias [d] of `weight_dtype` (MOE_F32 or `dtype`), each optional
+ *                (1 and 0 when NULL);
+ *   y [T, d] dense out; z [T, d] dense out, with a residual only;
+ *   stats [2, T] fp32 out: mu of every row, then r of every row, as the
+ *                backward reads them.
+ * Statistics and arithmetic are fp32; the statistics are those of the
+ * rounded z.  A row with a NaN or an infinity gives NaN; other rows do not
+ * notice.  Outputs must not overlap inputs.  Rows may start at any multiple
+ * of their element size; rows and strides in multiples of 16 bytes run
+ * fastest.  T == 0 enqueues nothing.
+ * Supported: 0 <= T < 2^31, 1 <= d <= 65536, eps >= 0, row strides >= d.
+ *
+ * moe_layer_norm_backward: the gradients for dy, the gradient of y, with n =
+ * (z - mu) r and g = dy * weight:
+ *   dx = round(r * (g - mean_j g - n mean_j(g n)) + dz)   [T, d] dense out
+ *   dweight = sum_t dy n,  dbias = sum_t dy               [d] fp32 out
+ *   dy, z, dz  rows of `dtype` with row strides as above; z is the forward's
+ *              z, or its x without a residual; dz optional: the gradient
+ *              that reaches z by the residual path;
+ *   stats      the forward's; weight as in the forward;
+ *   dweight, dbias  each optional; T == 0 sets them to zero.
+ * dx is the gradient of x and of the residual alike.  The sums over rows run
+ * over fixed sets of rows in a fixed order (no atomics).
+ * Workspace: moe_layer_norm_backward_workspace_bytes(T, d) bytes.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+MOE_API moe_status_t moe_layer_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                    const void* weight, const void* bias, int64_t T, int32_t d, int32_t dtype,
+                                    int32_t weight_dtype, float eps, void* y, void* z, float* stats,
+                                    moe_stream_t stream);
+MOE_API size_t moe_layer_norm_backward_workspace_bytes(int64_t T, int32_t d);
+MOE_API moe_status_t moe_layer_norm_backward(const void* dy, int64_t dy_stride, const void* z, int64_t z_stride,
+                                             const float* stats, const void* weight, const void* dz,
+                                             int64_t dz_stride, int64_t T, int32_t d, int32_t dtype,
+                                             int32_t weight_dtype, void* dx, float* dweight, float* dbias,
+                                             void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The router's auxiliary losses and their gradient ("Scalable Pretraining
+ * of Large MoE LMs on Aurora Super Computer": expert load-balancing
+ * auxiliary loss).  With p = softmax of a token's logits, lse its log-sum-
+ * exp, share_e = counts[e] / sum counts, and means over the N tokens that
+ * the mask keeps:
+ *   losses[0] = E * sum_e share_e mean_t p[t, e]     (1 when balanced)
+ *   losses[1] = mean_t lse_t^2
+ *   d_logits  = d_in + balance_coef d losses[0] + z_coef d losses[1]
+ * the shares held fixed (they count a discrete choice), so
+ *   d[t, e] = p[t, e] / N * (balance_coef E (share_e - sum_i p[t, i] share_i)
+ *                            + 2 z_coef lse_t).
+ *   logits [T, E] fp32; counts [E] int32 as moe_dispatch_scan writes them
+ *   (all zero: every share is zero); mask [T] bytes, optional: tokens whose
+ *   byte is 0 are left out (their logits are not read) and get no gradient;
+ *   d_in [T, E] fp32, optional, may be d_logits itself: the gradient that
+ *   is added to (moe_backward's d_logits); d_logits [T, E] fp32 out;
+ *   losses [2] fp32 out, without the coefficients.
+ * A logit of -infinity takes its expert out for that token; a token whose
+ * every logit is -infinity counts in N and contributes zero.  No token kept:
+ * losses and gradient are zero.  Softmax statistics and sums are fp32, the
+ * sums over blocks fp64.
+ * Workspace: moe_router_loss_workspace_bytes() bytes.
+ * Supported: 1 <= E <= 1024, 0 <= T, T*E < 2^40.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+MOE_API size_t moe_router_loss_workspace_bytes(void);
+MOE_API moe_status_t moe_router_loss(const float* logits, const int32_t* counts, const uint8_t* mask, int64_t T,
+                                     int32_t E, float balance_coef, float z_coef, const float* d_in,
+                                     float* d_logits, float* losses, void* workspace, size_t workspace_bytes,
+                                     moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over a list of tensors in one call.  Each tensor is described by a
+ * record in HOST memory (read before the call returns); its pointers are
+ * device memory:
+ *   param   n values of param_type, updated;
+ *   master  n fp32 values or NULL: when given, the step reads and writes the
+ *           master and param becomes its rounded copy;
+ *   grad    n values of grad_type;
+ *   m, v    the states.  state_bits 32: n fp32 values each (first moment,
+ *           second moment).  state_bits 8: n E4M3 codes each, of m and of
+ *           sqrt(v), with one fp32 scale for every 128 consecutive values
+ *           (the last block may be short) in m_scale and v_scale,
+ *           ceil(n / 128) entries each;
+ *   decay   multiplies the weight decay for this tensor (1, or 0 for norm
+ *           weights and biases).
+ * With g = grad * (*grad_scale, or 1), t the step:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p - (lr weight_decay decay p
+ *            + lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps))
+ * in fp32, with m and v used before they are rounded to 8 bits.  8-bit
+ * states: scale = amax / 448 over the block (1 when amax < 2^-100), code =
+ * E4M3(value * (448 / amax)), round to nearest even; a positive sqrt(v)
+ * keeps at least the smallest code, so that no denominator is lost to
+ * rounding.  The value is code * scale; all-zero codes with any finite scale
+ * are the initial state.  A NaN or an infinity in a gradient makes its block
+ * of 128 states NaN (its value only, with 32-bit states).
+ *   hyper       moe_adamw_hyper's record, in host memory; or NULL and
+ *   hyper_dev   the same record in device memory (a captured graph can be
+ *               replayed with new values written there);
+ *   grad_scale  device fp32, optional: moe_grad_norm's factor.  When it is
+ *               not finite the call changes nothing (the step is skipped).
+ * Tensors with n = 0 are skipped.  Tensors must not overlap.  A tensor whose
+ * pointers are 32-byte aligned runs fastest; the scales need 4-byte
+ * alignment, the rest that of their type.
+ *
+ * moe_adamw_hyper: the record for one step (host only, computed in fp64).
+ * Needs lr, weight_decay, eps >= 0, 0 <= beta < 1, step >= 1, all finite.
+ *
+ * moe_grad_norm: over the grad, grad_type and n of the same records,
+ *   out[0] = sqrt(sum of all squares)
+ *   out[1] = max_norm / out[0] when out[0] > max_norm, else 1; NaN when
+ *            out[0] is not finite (a gradient beyond about 1e19 counts as
+ *            infinite).  max_norm = infinity: never clipped.
+ *   Squares are summed in fp32 by each thread and in fp64 over threads, in a
+ *   fixed order.  Workspace: moe_grad_norm_workspace_bytes() bytes.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE, MOE_ERR_NO_DEVICE,
+ *         MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  int32_t param_type; /* moe_dtype_t */
+  int32_t grad_type;  /* moe_dtype_t */
+  int32_t state_bits; /* 32 or 8 */
+  float decay;
+} moe_adamw_tensor_t;
+
+typedef struct {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float step_size;     /* lr / (1 - beta1^step) */
+  float decay;         /* lr * weight_decay */
+  float inv_sqrt_bias; /* 1 / sqrt(1 - beta2^step) */
+  float eps;
+} moe_adamw_hyper_t;
+
+MOE_API moe_status_t moe_adamw_hyper(double lr, double beta1, double beta2, double eps, double weight_decay,
+                                     int64_t step, moe_adamw_hyper_t* hyper);
+MOE_API moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int32_t n_tensors,
+                                    const moe_adamw_hyper_t* hyper, const moe_adamw_hyper_t* hyper_dev,
+                                    const float* grad_scale, moe_stream_t stream);
+MOE_API size_t moe_grad_norm_workspace_bytes(void);
+MOE_API moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, float max_norm, float* out,
+                                   void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Check of the failure path every kernel shares: one block waits, with the

@@ -33,6 +33,19 @@ class ForwardLayout(ctypes.Structure):
                  "x_perm", "h", "y", "total")]
 
 
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t: one tensor of an optimizer list (device pointers)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("decay", ctypes.c_float)]
+
+
+class AdamWHyper(ctypes.Structure):
+    """moe_adamw_hyper_t: the coefficients of one step."""
+    _fields_ = [(n, ctypes.c_float) for n in
+                ("beta1", "one_minus_beta1", "beta2", "one_minus_beta2", "step_size", "decay", "inv_sqrt_bias", "eps")]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run sparse_expert_gb300/build.py (nvcc, sm_103a)")
 
@@ -42,6 +55,8 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+_D = ctypes.c_double
 _S = ctypes.c_int  # moe_status_t
 
 SIGNATURES = {
@@ -94,6 +109,16 @@ SIGNATURES = {
     "moe_backward": (_S, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_backward_timed": (_S, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P,
                                 _P]),
+    "moe_layer_norm": (_S, [_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I32, _I32, _F, _P, _P, _P, _P]),
+    "moe_layer_norm_backward_workspace_bytes": (_SZ, [_I64, _I32]),
+    "moe_layer_norm_backward": (_S, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _SZ,
+                                     _P]),
+    "moe_router_loss_workspace_bytes": (_SZ, []),
+    "moe_router_loss": (_S, [_P, _P, _P, _I64, _I32, _F, _F, _P, _P, _P, _P, _SZ, _P]),
+    "moe_adamw_hyper": (_S, [_D, _D, _D, _D, _D, _I64, ctypes.POINTER(AdamWHyper)]),
+    "moe_adamw_step": (_S, [_P, _I32, _P, _P, _P, _P]),
+    "moe_grad_norm_workspace_bytes": (_SZ, []),
+    "moe_grad_norm": (_S, [_P, _I32, _F, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)
@@ -661,3 +686,291 @@ def moe_dispatch_noalloc_status(stream=None) -> int:
     st = _I32(0)
     _check(lib.moe_dispatch_noalloc_status(_stream(stream), ctypes.byref(st)), "moe_dispatch_noalloc_status")
     return st.value
+
+
+# ------------------------------------------- the training step around the layer
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # moe_dtype_t
+
+
+def _raw_stream(stream):
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """Checks a [T, d] tensor of rows (unit stride along d) and returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'[T, d]' if shape is None else list(shape)}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.stride(0)
+
+
+def _norm_params(d, dtype, *params):
+    """Checks weight and bias (each [d] or None, of one type) and returns that type."""
+    wdt = None
+    for t, name in params:
+        if t is None:
+            continue
+        if t.dtype != torch.float32 and t.dtype != dtype:
+            raise TypeError(f"{name} must be float32 or {dtype}, got {t.dtype}")
+        if wdt is not None and t.dtype != wdt:
+            raise TypeError("weight and bias must have one type")
+        wdt = t.dtype
+        if t.shape != (d,):
+            raise ValueError(f"{name} must be [{d}], got {list(t.shape)}")
+        _contig(t, wdt, name)
+    return dtype if wdt is None else wdt
+
+
+def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, stats=None, z=None, stream=None):
+    """(y [T,d], stats [2,T]) of the rows of x [T,d] (any row stride), or
+    (y, stats, z) with a residual: z = x + residual, y = layer norm of z.
+    stats (mean, then reciprocal standard deviation) is what the backward reads."""
+    x_stride = _rows(x, "x")
+    T, d = x.shape
+    dt = x.dtype
+    wdt = _norm_params(d, dt, (weight, "weight"), (bias, "bias"))
+    r_stride = 0
+    if residual is not None:
+        r_stride = _rows(residual, "residual", x.shape, dt)
+        z = torch.empty(T, d, dtype=dt, device=x.device) if z is None else _out(z, x.shape, dt, "z")
+    elif z is not None:
+        raise ValueError("z is written with a residual only")
+    out = torch.empty(T, d, dtype=dt, device=x.device) if out is None else _out(out, x.shape, dt, "out")
+    if stats is None:
+        stats = torch.empty(2, T, dtype=torch.float32, device=x.device)
+    else:
+        _out(stats, (2, T), torch.float32, "stats")
+    _check(lib.moe_layer_norm(x.data_ptr(), x_stride, residual.data_ptr() if residual is not None else None, r_stride,
+                              weight.data_ptr() if weight is not None else None,
+                              bias.data_ptr() if bias is not None else None, T, d, _DTYPES[dt], _DTYPES[wdt], eps,
+                              out.data_ptr(), z.data_ptr() if z is not None else None, stats.data_ptr(),
+                              _raw_stream(stream)), "moe_layer_norm")
+    return (out, stats) if residual is None else (out, stats, z)
+
+
+def _out(t, shape, dtype, name):
+    _contig(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def moe_layer_norm_backward_workspace_bytes(T, d) -> int:
+    return lib.moe_layer_norm_backward_workspace_bytes(T, d)
+
+
+def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads=None, workspace=None, stream=None):
+    """dict(dx, dweight, dbias) for the gradient dy of moe_layer_norm's output.
+    z: its z, or its x without a residual; dz: the gradient that reaches z by
+    the residual path, added to dx.  dweight is None without a weight, dbias
+    with bias=False.  grads: such a dict to write into."""
+    dy_stride = _rows(dy, "dy")
+    T, d = dy.shape
+    dt, dev = dy.dtype, dy.device
+    z_stride = _rows(z, "z", dy.shape, dt)
+    wdt = _norm_params(d, dt, (weight, "weight"))
+    _out(stats, (2, T), torch.float32, "stats")
+    dz_stride = _rows(dz, "dz", dy.shape, dt) if dz is not None else 0
+    if grads is None:
+        sums = torch.empty(2, d, dtype=torch.float32, device=dev)
+        grads = dict(dx=torch.empty(T, d, dtype=dt, device=dev), dweight=sums[0] if weight is not None else None,
+                     dbias=sums[1] if bias else None)
+    else:
+        _out(grads["dx"], dy.shape, dt, "dx")
+        for name in ("dweight", "dbias"):
+            if grads[name] is not None:
+                _out(grads[name], (d,), torch.float32, name)
+    dw, db = grads["dweight"], grads["dbias"]
+    if workspace is None:
+        workspace = torch.empty(lib.moe_layer_norm_backward_workspace_bytes(T, d), dtype=torch.uint8, device=dev)
+    _check(lib.moe_layer_norm_backward(dy.data_ptr(), dy_stride, z.data_ptr(), z_stride, stats.data_ptr(),
+                                       weight.data_ptr() if weight is not None else None,
+                                       dz.data_ptr() if dz is not None else None, dz_stride, T, d, _DTYPES[dt],
+                                       _DTYPES[wdt], grads["dx"].data_ptr(), dw.data_ptr() if dw is not None else None,
+                                       db.data_ptr() if db is not None else None, workspace.data_ptr(),
+                                       workspace.numel(), _raw_stream(stream)), "moe_layer_norm_backward")
+    return grads
+
+
+def moe_router_loss(logits, counts, balance_coef=0.01, z_coef=0.001, mask=None, accumulate=None, out=None, losses=None,
+                    workspace=None, stream=None):
+    """(losses [2], d_logits [T,E]) of the router's load-balancing loss and
+    z-loss (both without their coefficients) and the gradient of
+    balance_coef * losses[0] + z_coef * losses[1].
+    counts [E] int32: the tokens each expert received; mask [T] bool: tokens
+    to count; accumulate: a [T,E] gradient that this one is added to, in
+    place (moe_backward's d_logits)."""
+    _contig(logits, torch.float32, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    _out(counts, (E,), torch.int32, "counts")
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
+        _out(mask, (T,), mask.dtype, "mask")
+    if accumulate is not None:
+        _out(accumulate, logits.shape, torch.float32, "accumulate")
+        if out is not None:
+            raise ValueError("accumulate is written in place: give it or out")
+        out = accumulate
+    elif out is None:
+        out = torch.empty(T, E, dtype=torch.float32, device=dev)
+    else:
+        _out(out, logits.shape, torch.float32, "out")
+    if losses is None:
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+    else:
+        _out(losses, (2,), torch.float32, "losses")
+    if workspace is None:
+        workspace = torch.empty(lib.moe_router_loss_workspace_bytes(), dtype=torch.uint8, device=dev)
+    _check(lib.moe_router_loss(logits.data_ptr(), counts.data_ptr(), mask.data_ptr() if mask is not None else None, T,
+                               E, balance_coef, z_coef, accumulate.data_ptr() if accumulate is not None else None,
+                               out.data_ptr(), losses.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                               _raw_stream(stream)), "moe_router_loss")
+    return losses, out
+
+
+class TensorList:
+    """The records of a list of tensors for moe_grad_norm and moe_adamw_step
+    (made by moe_tensor_list or moe_adamw_plan), and the tensors themselves,
+    so that the records' pointers stay valid."""
+
+    def __init__(self, records, tensors, device, has_states):
+        self.records, self.tensors, self.device, self.has_states = records, tensors, device, has_states
+
+    def __len__(self):
+        return len(self.records)
+
+
+def _flat(t, name, dtypes, n=None, device=None):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} values, got {t.numel()}")
+    return t
+
+
+def moe_tensor_list(grads) -> TensorList:
+    """The list of gradients (contiguous, fp32, bf16 or fp16) for moe_grad_norm."""
+    grads = list(grads)
+    records = (AdamWTensor * len(grads))()
+    for r, g in zip(records, grads):
+        _flat(g, "a gradient", _DTYPES, None, grads[0].device)
+        r.grad, r.n, r.grad_type = g.data_ptr(), g.numel(), _DTYPES[g.dtype]
+    return TensorList(records, grads, grads[0].device if grads else None, False)
+
+
+def moe_adamw_state(params, bits=32):
+    """Zero states for moe_adamw_plan, as a dict of its arguments m, v,
+    m_scales and v_scales: fp32 values, or 8-bit codes and their scales."""
+    if bits not in (32, 8):
+        raise ValueError("bits must be 32 or 8")
+    dt = torch.float32 if bits == 32 else torch.uint8
+
+    def zeros():
+        return [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params]
+
+    def scales():
+        return [torch.ones(-(-p.numel() // 128), dtype=torch.float32, device=p.device) if bits == 8 else None
+                for p in params]
+    return dict(m=zeros(), v=zeros(), m_scales=scales(), v_scales=scales())
+
+
+def moe_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, masters=None, decay=None) -> TensorList:
+    """The list of tensors for moe_adamw_step and moe_grad_norm, made once.
+
+    params and grads are fp32, bf16 or fp16; m and v are fp32, or uint8 codes
+    with fp32 scales for every 128 values (mixed lists are fine); masters:
+    fp32 masters (an entry may be None); decay: factor on the weight decay of
+    each tensor (default 1).  The plan holds pointers to these tensors: make a
+    new one when a tensor is replaced by another."""
+    n_tensors = len(params)
+    m_scales, v_scales, masters = (([None] * n_tensors) if a is None else a for a in (m_scales, v_scales, masters))
+    decay = [1.0] * n_tensors if decay is None else decay
+    every = (params, grads, m, v, m_scales, v_scales, masters, decay)
+    if any(len(a) != n_tensors for a in every):
+        raise ValueError("the lists must have one entry for each parameter")
+    records = (AdamWTensor * n_tensors)()
+    device = params[0].device if n_tensors else None
+    for r, p, g, mm, vv, ms, vs, master, wd in zip(records, *every):
+        _flat(p, "a parameter", _DTYPES, None, device)
+        n = p.numel()
+        _flat(g, "a gradient", _DTYPES, n, device)
+        _flat(mm, "m", (torch.float32, torch.uint8), n, device)
+        _flat(vv, "v", (mm.dtype,), n, device)
+        r.param, r.grad, r.m, r.v, r.n = p.data_ptr(), g.data_ptr(), mm.data_ptr(), vv.data_ptr(), n
+        r.param_type, r.grad_type = _DTYPES[p.dtype], _DTYPES[g.dtype]
+        r.state_bits = 32 if mm.dtype == torch.float32 else 8
+        if r.state_bits == 8:
+            if ms is None or vs is None:
+                raise ValueError("8-bit states need m_scales and v_scales")
+            r.m_scale = _flat(ms, "m_scales", (torch.float32,), -(-n // 128), device).data_ptr()
+            r.v_scale = _flat(vs, "v_scales", (torch.float32,), -(-n // 128), device).data_ptr()
+        if master is not None:
+            r.master = _flat(master, "a master", (torch.float32,), n, device).data_ptr()
+        r.decay = wd
+    return TensorList(records, every, device, True)
+
+
+def moe_grad_norm(tensors, max_norm=float("inf"), out=None, workspace=None, stream=None):
+    """[norm, factor] (fp32, on the device) over all gradients of a plan, a
+    moe_tensor_list or a sequence of tensors; factor = max_norm / norm where
+    the norm is larger, else 1 (NaN for a norm that is not finite): the `clip`
+    argument of moe_adamw_step."""
+    if not isinstance(tensors, TensorList):
+        tensors = moe_tensor_list(tensors)
+    device = tensors.device if tensors.device is not None else torch.device("cuda", torch.cuda.current_device())
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=device)
+    else:
+        _out(out, (2,), torch.float32, "out")
+    if workspace is None:
+        workspace = torch.empty(lib.moe_grad_norm_workspace_bytes(), dtype=torch.uint8, device=device)
+    _check(lib.moe_grad_norm(tensors.records, len(tensors.records), max_norm, out.data_ptr(), workspace.data_ptr(),
+                             workspace.numel(), _raw_stream(stream)), "moe_grad_norm")
+    return out
+
+
+def moe_adamw_hyper(lr, step, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1):
+    """The coefficients of one step as 8 fp32 values on the host: copied into
+    a device tensor, they are moe_adamw_step's `hyper` (for captured graphs)."""
+    h = AdamWHyper()
+    _check(lib.moe_adamw_hyper(lr, betas[0], betas[1], eps, weight_decay, step, ctypes.byref(h)), "moe_adamw_hyper")
+    return torch.frombuffer(bytearray(h), dtype=torch.float32)
+
+
+def moe_adamw_step(plan, lr=None, step=None, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, clip=None, hyper=None,
+                   stream=None):
+    """One AdamW step over the tensors of a plan, in place.  step counts from
+    1; clip: moe_grad_norm's output (its second value multiplies the
+    gradients; the step is skipped when that is not finite); hyper: device
+    coefficients from moe_adamw_hyper, in place of lr, step, betas, eps and
+    weight_decay."""
+    if not plan.has_states:
+        raise ValueError("moe_adamw_step needs a plan from moe_adamw_plan")
+    scale = None
+    if clip is not None:
+        scale = _out(clip, (2,), torch.float32, "clip").data_ptr() + 4
+    if hyper is not None:
+        if lr is not None or step is not None:
+            raise ValueError("give hyper, or lr and step")
+        host, dev = None, _out(hyper, (8,), torch.float32, "hyper").data_ptr()
+    else:
+        if lr is None or step is None:
+            raise ValueError("lr and step are needed without hyper")
+        h = AdamWHyper()
+        _check(lib.moe_adamw_hyper(lr, betas[0], betas[1], eps, weight_decay, step, ctypes.byref(h)), "moe_adamw_hyper")
+        host, dev = ctypes.addressof(h), None
+    _check(lib.moe_adamw_step(plan.records, len(plan.records), host, dev, scale, _raw_stream(stream)),
+           "moe_adamw_step")

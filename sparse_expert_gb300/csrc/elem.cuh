@@ -1,0 +1,87 @@
+// Element types of the training-step kernels (layer norm, optimizer): fp32,
+// bf16 and fp16 values read from memory, computed on in fp32, rounded to
+// nearest even when stored.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// One 32-bit word holds one fp32 value or two 16-bit ones.
+template <typename T>
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr int kValues = 1;
+  __device__ static __forceinline__ void unpack(uint32_t u, float* v) { v[0] = __uint_as_float(u); }
+  __device__ static __forceinline__ uint32_t pack(const float* v) { return __float_as_uint(v[0]); }
+};
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr int kValues = 2;
+  __device__ static __forceinline__ void unpack(uint32_t u, float* v) {
+    v[0] = __uint_as_float(u << 16);
+    v[1] = __uint_as_float(u & 0xffff0000u);
+  }
+  __device__ static __forceinline__ uint32_t pack(const float* v) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+};
+template <>
+struct Word<__half> {
+  static constexpr int kValues = 2;
+  __device__ static __forceinline__ void unpack(uint32_t u, float* v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    v[0] = f.x;
+    v[1] = f.y;
+  }
+  __device__ static __forceinline__ uint32_t pack(const float* v) {
+    const __half2 p = __floats2half2_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+};
+
+// The 16 bytes of a chunk as fp32 values, and back.
+template <typename T>
+constexpr int kChunk = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+__device__ __forceinline__ void unpack_chunk(const uint4& u, float* v) {
+  constexpr int k = Word<T>::kValues;
+  Word<T>::unpack(u.x, v);
+  Word<T>::unpack(u.y, v + k);
+  Word<T>::unpack(u.z, v + 2 * k);
+  Word<T>::unpack(u.w, v + 3 * k);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_chunk(const float* v) {
+  constexpr int k = Word<T>::kValues;
+  return make_uint4(Word<T>::pack(v), Word<T>::pack(v + k), Word<T>::pack(v + 2 * k), Word<T>::pack(v + 3 * k));
+}
+
+// Sum over the aligned group of `width` (a power of two up to 32) lanes that
+// the calling lane belongs to, the same value on each.
+__device__ __forceinline__ float group_sum(float v, int width) {
+  for (int s = width >> 1; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  return v;
+}
+
+}  // namespace moe

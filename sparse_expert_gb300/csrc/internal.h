@@ -234,6 +234,69 @@ bool make_bf16_map_col_blocks(CUtensorMap* map, const void* ptr, int64_t rows, i
 // swizzle: 16-byte piece c of row r lands at piece c ^ ((r >> 1) & 3).
 bool make_u8_map_rows64_sw64(CUtensorMap* map, const void* ptr, int64_t rows, int box_rows);
 
+// ---- the training step around the layer
+constexpr int kNormMaxBlocks = 512;  // blocks of the layer norm backward, so partial column sums
+struct NormForward {
+  const void* x;
+  int64_t x_stride;  // elements between rows
+  const void* residual;
+  int64_t residual_stride;
+  const void* weight;
+  const void* bias;
+  int64_t T;
+  int d;
+  int dtype, weight_dtype;  // moe_dtype_t
+  float eps;
+  void* y;
+  void* z;       // with a residual: round(x + residual)
+  float* stats;  // [2][T]: mean, reciprocal standard deviation
+};
+cudaError_t launch_layer_norm(const NormForward& f, cudaStream_t stream);
+struct NormBackward {
+  const void* dy;
+  int64_t dy_stride;
+  const void* z;
+  int64_t z_stride;
+  const float* stats;
+  const void* weight;
+  const void* dz;
+  int64_t dz_stride;
+  int64_t T;
+  int d;
+  int dtype, weight_dtype;
+  void* dx;
+  float* dweight;  // [d] or null
+  float* dbias;    // [d] or null
+  float* partial;  // norm_backward_workspace_bytes(T, d)
+};
+size_t norm_backward_workspace_bytes(int64_t T, int d);
+cudaError_t launch_layer_norm_backward(const NormBackward& f, int num_sms, cudaStream_t stream);
+
+// The router's auxiliary losses and their gradient.
+struct RouterLoss {
+  const float* logits;    // [T, E]
+  const int32_t* counts;  // [E]
+  const uint8_t* mask;    // [T] or null
+  int64_t T;
+  int E;
+  float balance_coef, z_coef;
+  const float* d_in;      // [T, E] added to the gradient, or null (may be d_logits)
+  float* d_logits;        // [T, E]
+  float* losses;          // [2]
+  float* partial;         // router_loss_workspace_bytes()
+};
+constexpr int kRouterLossMaxBlocks = 1024;
+size_t router_loss_workspace_bytes();
+cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream);
+
+// The optimizer's lists of tensors (arrays in host memory).
+constexpr int kGradNormMaxBlocks = 2048;
+size_t grad_norm_workspace_bytes();
+cudaError_t launch_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out,
+                             double* partial, int num_sms, cudaStream_t stream);
+cudaError_t launch_adamw(const moe_adamw_tensor_t* tensors, int n_tensors, const moe_adamw_hyper_t* hyper,
+                         const moe_adamw_hyper_t* hyper_dev, const float* grad_scale, cudaStream_t stream);
+
 // Bounded-wait check: one block waits on a phase that never completes and
 // records a timeout in *status after limit_ns.
 cudaError_t launch_wait_timeout(int32_t* status, uint64_t limit_ns, cudaStream_t stream);

@@ -1,0 +1,305 @@
+// AdamW over a list of tensors, and the norm of a list of gradients.
+//
+//   g = grad * factor;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p - (lr wd p + lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps))
+//
+// The list travels in the kernel's parameters (up to 32 KB), so a call is one
+// launch per kCapacity tensors, needs no copy to the device, keeps nothing
+// from call to call and can be captured into a graph.  The tensors are cut
+// into chunks of kChunkValues values; chunks are numbered through the list,
+// and a block finds its tensor by bisection of the first chunk numbers.
+//
+// 8-bit states: m and sqrt(v) as E4M3 codes with one fp32 scale per 128
+// values.  sqrt(v) and not v: E4M3 spans a ratio of 2^18 (to a sixteenth of
+// the value or better above 2^-15 of the maximum), which as v itself is 2^36.
+// The products and sums of m and v are rounded one by one (no fused
+// multiply-add), so that the codes do not depend on how they are contracted.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kScaleBlock = 128;
+constexpr int kChunkValues = 4096;
+constexpr float kE4M3Max = 448.0f;
+constexpr float kTinyBlock = 7.888609052210118e-31f;  // 2^-100
+
+struct Tensor {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float decay;
+  uint8_t param_type, grad_type, bits8, vec;  // vec: whole vectors at aligned addresses
+};
+
+template <int kCapacity>
+struct List {
+  int count;
+  int chunks;
+  moe_adamw_hyper_t hyper;
+  const moe_adamw_hyper_t* hyper_dev;
+  const float* grad_scale;
+  int first[kCapacity + 1];  // number of each tensor's first chunk
+  Tensor t[kCapacity];
+};
+
+// The tensor of a chunk: the last one whose first chunk is not after it
+// (tensors without values are not in the list).
+template <int kCapacity>
+__device__ __forceinline__ int tensor_of(const List<kCapacity>& list, int chunk) {
+  int lo = 0, hi = list.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (list.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float load_any(const void* p, int type, int64_t i) {
+  if (type == MOE_F32) return static_cast<const float*>(p)[i];
+  if (type == MOE_BF16) return to_f32(static_cast<const __nv_bfloat16*>(p)[i]);
+  return to_f32(static_cast<const __half*>(p)[i]);
+}
+
+__device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v) {
+  if (type == MOE_F32) static_cast<float*>(p)[i] = v;
+  else if (type == MOE_BF16) static_cast<__nv_bfloat16*>(p)[i] = from_f32<__nv_bfloat16>(v);
+  else static_cast<__half*>(p)[i] = from_f32<__half>(v);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float decode(uint8_t code, float scale) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
+  return __fmul_rn(__half2float(__half(h)), scale);
+}
+
+// The scale of a block with maximum `amax`, and the factor into the codes.
+__device__ __forceinline__ void block_scale(float amax, float* scale, float* inv) {
+  const bool tiny = amax < kTinyBlock;  // not for NaN: it spreads to the block
+  *scale = tiny ? 1.0f : __fmul_rn(amax, 1.0f / kE4M3Max);
+  *inv = tiny ? 1.0f : __fdiv_rn(kE4M3Max, amax);
+}
+
+// Products and sums rounded singly; the new moments and the new parameter.
+__device__ __forceinline__ void adamw_value(const moe_adamw_hyper_t& h, float decay, float g, float& p, float& m,
+                                            float& v, float& root) {
+  m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.one_minus_beta1));
+  v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.one_minus_beta2));
+  root = __fsqrt_rn(v);
+  const float update = __fdiv_rn(m * h.step_size, root * h.inv_sqrt_bias + h.eps);
+  p = p - (p * decay + update);
+}
+
+template <int kCapacity>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
+  const moe_adamw_hyper_t h = list.hyper_dev ? *list.hyper_dev : list.hyper;
+  const float factor = list.grad_scale ? *list.grad_scale : 1.0f;
+  if (!isfinite(factor)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int which = tensor_of(list, blockIdx.x);
+  const Tensor& t = list.t[which];
+  const float decay = h.decay * t.decay;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[which]) * kChunkValues;
+  // a warp takes blocks of 128 values, lane + 32 i of each
+  for (int64_t b0 = begin + warp * kScaleBlock; b0 < t.n && b0 < begin + kChunkValues;
+       b0 += kScaleBlock * (kThreads / 32)) {
+    const int64_t block = b0 / kScaleBlock;
+    const float ms = t.bits8 ? t.m_scale[block] : 1.0f, vs = t.bits8 ? t.v_scale[block] : 1.0f;
+    float m[4], root[4];
+    float m_max = 0.0f, v_max = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = b0 + lane + 32 * i;
+      m[i] = root[i] = 0.0f;
+      if (j >= t.n) continue;
+      const float g = __fmul_rn(load_any(t.grad, t.grad_type, j), factor);
+      float p = t.master ? t.master[j] : load_any(t.param, t.param_type, j);
+      float v;
+      if (t.bits8) {
+        m[i] = decode(static_cast<const uint8_t*>(t.m)[j], ms);
+        v = decode(static_cast<const uint8_t*>(t.v)[j], vs);
+        v = __fmul_rn(v, v);
+      } else {
+        m[i] = static_cast<const float*>(t.m)[j];
+        v = static_cast<const float*>(t.v)[j];
+      }
+      adamw_value(h, decay, g, p, m[i], v, root[i]);
+      if (t.master) t.master[j] = p;
+      store_any(t.param, t.param_type, j, p);
+      if (!t.bits8) {
+        static_cast<float*>(t.m)[j] = m[i];
+        static_cast<float*>(t.v)[j] = v;
+      }
+      m_max = max_nan(m_max, fabsf(m[i]));
+      v_max = max_nan(v_max, root[i]);
+    }
+    if (!t.bits8) continue;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+      m_max = max_nan(m_max, __shfl_xor_sync(0xffffffffu, m_max, s));
+      v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, s));
+    }
+    float m_scale, m_inv, v_scale, v_inv;
+    block_scale(m_max, &m_scale, &m_inv);
+    block_scale(v_max, &v_scale, &v_inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = b0 + lane + 32 * i;
+      if (j >= t.n) continue;
+      static_cast<uint8_t*>(t.m)[j] = __nv_cvt_float_to_fp8(__fmul_rn(m[i], m_inv), __NV_SATFINITE, __NV_E4M3);
+      uint8_t code = __nv_cvt_float_to_fp8(__fmul_rn(root[i], v_inv), __NV_SATFINITE, __NV_E4M3);
+      if (code == 0 && root[i] > 0.0f) code = 1;
+      static_cast<uint8_t*>(t.v)[j] = code;
+    }
+    if (lane == 0) {
+      t.m_scale[block] = m_scale;
+      t.v_scale[block] = v_scale;
+    }
+  }
+}
+
+// ---- gradient norm
+__device__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double total = 0.0;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kThreads / 32; ++i) total += red[i];
+  return total;
+}
+
+template <int kCapacity>
+__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ List<kCapacity> list,
+                                                           double* __restrict__ partial) {
+  __shared__ double red[kThreads / 32];
+  float s = 0.0f;
+  for (int chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
+    const int which = tensor_of(list, chunk);
+    const Tensor& t = list.t[which];
+    const int64_t begin = static_cast<int64_t>(chunk - list.first[which]) * kChunkValues;
+    const int64_t end = begin + kChunkValues < t.n ? begin + kChunkValues : t.n;
+    for (int64_t j = begin + threadIdx.x; j < end; j += kThreads) {
+      const float g = load_any(t.grad, t.grad_type, j);
+      s += g * g;
+    }
+  }
+  const double total = block_sum(s, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict__ partial, int blocks, float max_norm,
+                                                        float* __restrict__ out) {
+  __shared__ double red[kThreads / 32];
+  double s = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += kThreads) s += partial[b];
+  s = block_sum(s, red);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(s);
+    out[0] = static_cast<float>(norm);
+    out[1] = !isfinite(out[0]) ? nanf("") : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.0f;
+  }
+}
+
+// ---- lists
+template <int kCapacity>
+int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, int* at) {
+  list.count = 0;
+  int64_t chunks = 0;
+  while (*at < n_tensors && list.count < kCapacity) {
+    const moe_adamw_tensor_t& s = tensors[*at];
+    const int64_t more = (s.n + kChunkValues - 1) / kChunkValues;
+    if (chunks + more > INT32_MAX) break;
+    ++*at;
+    if (s.n == 0) continue;
+    list.first[list.count] = static_cast<int>(chunks);
+    list.t[list.count++] = Tensor{s.param, s.master, s.grad, s.m, s.v, s.m_scale, s.v_scale, s.n, s.decay,
+                                  static_cast<uint8_t>(s.param_type), static_cast<uint8_t>(s.grad_type),
+                                  static_cast<uint8_t>(s.state_bits == 8), 0};
+    chunks += more;
+  }
+  list.chunks = static_cast<int>(chunks);
+  return list.chunks;
+}
+
+template <int kCapacity>
+cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const moe_adamw_hyper_t* hyper,
+                      const moe_adamw_hyper_t* hyper_dev, const float* grad_scale, cudaStream_t stream) {
+  List<kCapacity> list;
+  if (hyper) list.hyper = *hyper;
+  list.hyper_dev = hyper_dev;
+  list.grad_scale = grad_scale;
+  for (int at = 0; at < n_tensors;) {
+    if (fill(list, tensors, n_tensors, &at) == 0) continue;
+    adamw_kernel<kCapacity><<<list.chunks, kThreads, 0, stream>>>(list);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+template <int kCapacity>
+cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out, double* partial,
+                     int num_sms, cudaStream_t stream) {
+  List<kCapacity> list{};
+  const int launches = (n_tensors + kCapacity - 1) / kCapacity;
+  int most = num_sms * 8;
+  if (launches > 0 && most > kGradNormMaxBlocks / launches) most = kGradNormMaxBlocks / launches;
+  if (most < 1) return cudaErrorInvalidValue;
+  int blocks = 0;
+  for (int at = 0; at < n_tensors;) {
+    const int chunks = fill(list, tensors, n_tensors, &at);
+    if (chunks == 0) continue;
+    const int grid = chunks < most ? chunks : most;
+    if (blocks + grid > kGradNormMaxBlocks) return cudaErrorInvalidValue;
+    squares_kernel<kCapacity><<<grid, kThreads, 0, stream>>>(list, partial + blocks);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    blocks += grid;
+  }
+  norm_kernel<<<1, kThreads, 0, stream>>>(partial, blocks, max_norm, out);
+  return cudaGetLastError();
+}
+
+// Capacities of the kernels' lists: a call takes the smallest that holds its
+// tensors (a launch copies the whole list), and as many launches of the
+// largest as a longer list needs.
+constexpr int kSmallList = 8, kMediumList = 48, kLargeList = 384;
+static_assert(sizeof(List<kLargeList>) <= 32764, "kernel parameters");
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes() { return align_up(kGradNormMaxBlocks * sizeof(double)); }
+
+cudaError_t launch_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out,
+                             double* partial, int num_sms, cudaStream_t stream) {
+  if (n_tensors <= kSmallList) return norm_all<kSmallList>(tensors, n_tensors, max_norm, out, partial, num_sms, stream);
+  if (n_tensors <= kMediumList) return norm_all<kMediumList>(tensors, n_tensors, max_norm, out, partial, num_sms, stream);
+  return norm_all<kLargeList>(tensors, n_tensors, max_norm, out, partial, num_sms, stream);
+}
+
+cudaError_t launch_adamw(const moe_adamw_tensor_t* tensors, int n_tensors, const moe_adamw_hyper_t* hyper,
+                         const moe_adamw_hyper_t* hyper_dev, const float* grad_scale, cudaStream_t stream) {
+  if (n_tensors <= kSmallList) return adamw_all<kSmallList>(tensors, n_tensors, hyper, hyper_dev, grad_scale, stream);
+  if (n_tensors <= kMediumList) return adamw_all<kMediumList>(tensors, n_tensors, hyper, hyper_dev, grad_scale, stream);
+  return adamw_all<kLargeList>(tensors, n_tensors, hyper, hyper_dev, grad_scale, stream);
+}
+
+}  // namespace moe
