@@ -186,7 +186,7 @@ moe_status_t moe_router_loss(const float* logits, const int32_t* counts, const u
     return fail(MOE_ERR_WORKSPACE, "the workspace must hold moe_router_loss_workspace_bytes, 256-byte aligned");
   if ((s = device_info(&dev)) != MOE_OK) return s;
   const cudaError_t e = launch_router_loss(RouterLoss{logits, counts, mask, T, E, balance_coef, z_coef, d_in, d_logits,
-                                                      losses, static_cast<float*>(workspace)},
+                                                      losses, workspace},
                                            dev.num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "router loss launch");
 }

@@ -283,7 +283,7 @@ struct RouterLoss {
   const float* d_in;      // [T, E] added to the gradient, or null (may be d_logits)
   float* d_logits;        // [T, E]
   float* losses;          // [2]
-  float* partial;         // router_loss_workspace_bytes()
+  void* workspace;        // router_loss_workspace_bytes()
 };
 constexpr int kRouterLossMaxBlocks = 1024;
 size_t router_loss_workspace_bytes();

@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kScaleBlock = 128;
-constexpr int kChunkValues = 4096;
+constexpr int kChunkValues = kThreads * 8;       // one vector a thread
+constexpr int kNormChunkValues = kThreads * 32;  // four
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTinyBlock = 7.888609052210118e-31f;  // 2^-100
 
@@ -78,6 +79,54 @@ __device__ __forceinline__ void store_any(void* p, int type, int64_t i, float v)
   else static_cast<__half*>(p)[i] = from_f32<__half>(v);
 }
 
+// Eight values of a thread: 32 bytes of fp32 in one access, 16 bytes of a
+// 16-bit type, kept as they are until every load of the thread is on its way.
+struct Raw8 {
+  uint32_t w[8];
+};
+
+__device__ __forceinline__ void load8_f32(const float* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ void store8_f32(float* p, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void load8(const void* p, int type, int64_t i, Raw8& r) {
+  if (type == MOE_F32) {
+    load8_f32(static_cast<const float*>(p) + i, r.w);
+  } else {
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(static_cast<const uint16_t*>(p) + i));
+  }
+}
+
+__device__ __forceinline__ void values8(const Raw8& r, int type, float (&v)[8]) {
+  if (type == MOE_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+  } else {
+    const uint4 u = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    if (type == MOE_BF16) unpack_chunk<__nv_bfloat16>(u, v);
+    else unpack_chunk<__half>(u, v);
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, int type, int64_t i, const float (&v)[8]) {
+  if (type == MOE_F32) {
+    store8_f32(static_cast<float*>(p) + i, v);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+        type == MOE_BF16 ? pack_chunk<__nv_bfloat16>(v) : pack_chunk<__half>(v);
+  }
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -102,21 +151,118 @@ __device__ __forceinline__ void adamw_value(const moe_adamw_hyper_t& h, float de
   m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.one_minus_beta1));
   v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.one_minus_beta2));
   root = __fsqrt_rn(v);
-  const float update = __fdiv_rn(m * h.step_size, root * h.inv_sqrt_bias + h.eps);
+  // the quotient goes into a sum that rounds away far more than its two ulps
+  const float update = __fdividef(m * h.step_size, root * h.inv_sqrt_bias + h.eps);
   p = p - (p * decay + update);
 }
 
-template <int kCapacity>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
-  const moe_adamw_hyper_t h = list.hyper_dev ? *list.hyper_dev : list.hyper;
-  const float factor = list.grad_scale ? *list.grad_scale : 1.0f;
+// E4M3 codes of eight values, four to a word.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 lo = make_float2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv));
+    const float2 hi = make_float2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv));
+    w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
+           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void decode8(const uint2& codes, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t word = i < 2 ? codes.x : codes.y;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(word >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = __fmul_rn(f.x, scale);
+    v[2 * i + 1] = __fmul_rn(f.y, scale);
+  }
+}
+
+// A whole chunk of a tensor with aligned pointers: eight consecutive values
+// a thread, so sixteen lanes hold the 128 values of a scale.
+template <bool kBits8>
+__device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
+                                            int64_t begin) {
+  const int64_t j = begin + threadIdx.x * 8;
+  Raw8 raw_g, raw_p, raw_m, raw_v;
+  uint2 code_m, code_v;
+  float ms, vs;
+  load8(t.grad, t.grad_type, j, raw_g);
+  const bool master = t.master != nullptr;
+  const int p_type = master ? static_cast<int>(MOE_F32) : t.param_type;
+  load8(master ? t.master : t.param, p_type, j, raw_p);
+  if (kBits8) {
+    code_m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
+    code_v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
+    ms = t.m_scale[j / kScaleBlock];
+    vs = t.v_scale[j / kScaleBlock];
+  } else {
+    load8_f32(static_cast<const float*>(t.m) + j, raw_m.w);
+    load8_f32(static_cast<const float*>(t.v) + j, raw_v.w);
+  }
+  const float factor = factor_p ? *factor_p : 1.0f;
+  if (!isfinite(factor)) return;
+  const float decay = h.decay * t.decay;
+  float g[8], p[8], m[8], v[8], root[8];
+  values8(raw_g, t.grad_type, g);
+  values8(raw_p, p_type, p);
+  if (kBits8) {
+    decode8(code_m, ms, m);
+    decode8(code_v, vs, v);
+  }
+  float m_max = 0.0f, v_max = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (kBits8) {
+      v[i] = __fmul_rn(v[i], v[i]);
+    } else {
+      m[i] = __uint_as_float(raw_m.w[i]);
+      v[i] = __uint_as_float(raw_v.w[i]);
+    }
+    adamw_value(h, decay, __fmul_rn(g[i], factor), p[i], m[i], v[i], root[i]);
+    m_max = max_nan(m_max, fabsf(m[i]));
+    v_max = max_nan(v_max, root[i]);
+  }
+  if (master) store8_f32(t.master + j, p);
+  store8(t.param, t.param_type, j, p);
+  if (!kBits8) {
+    store8_f32(static_cast<float*>(t.m) + j, m);
+    store8_f32(static_cast<float*>(t.v) + j, v);
+    return;
+  }
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) {
+    m_max = max_nan(m_max, __shfl_xor_sync(0xffffffffu, m_max, s));
+    v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, s));
+  }
+  float m_scale, m_inv, v_scale, v_inv;
+  block_scale(m_max, &m_scale, &m_inv);
+  block_scale(v_max, &v_scale, &v_inv);
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = encode8(m, m_inv);
+  uint2 codes = encode8(root, v_inv);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t& w = i < 4 ? codes.x : codes.y;
+    const uint32_t one = 1u << (8 * (i & 3));
+    if ((w & (one * 255u)) == 0 && root[i] > 0.0f) w |= one;
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
+  if ((threadIdx.x & 15) == 0) {
+    t.m_scale[j / kScaleBlock] = m_scale;
+    t.v_scale[j / kScaleBlock] = v_scale;
+  }
+}
+
+// The last, partial chunk of a tensor, and every chunk of a tensor with
+// other pointers: a warp takes blocks of 128 values, lane + 32 i of each.
+__device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
+                                                   int64_t begin) {
+  const float factor = factor_p ? *factor_p : 1.0f;
   if (!isfinite(factor)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int which = tensor_of(list, blockIdx.x);
-  const Tensor& t = list.t[which];
   const float decay = h.decay * t.decay;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[which]) * kChunkValues;
-  // a warp takes blocks of 128 values, lane + 32 i of each
   for (int64_t b0 = begin + warp * kScaleBlock; b0 < t.n && b0 < begin + kChunkValues;
        b0 += kScaleBlock * (kThreads / 32)) {
     const int64_t block = b0 / kScaleBlock;
@@ -174,6 +320,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
 }
 
+template <int kCapacity>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
+  const moe_adamw_hyper_t h = list.hyper_dev ? *list.hyper_dev : list.hyper;
+  const int which = tensor_of(list, blockIdx.x);
+  const Tensor& t = list.t[which];
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[which]) * kChunkValues;
+  if (!t.vec || begin + kChunkValues > t.n) adamw_scalar_chunk(t, h, list.grad_scale, begin);
+  else if (t.bits8) adamw_chunk<true>(t, h, list.grad_scale, begin);
+  else adamw_chunk<false>(t, h, list.grad_scale, begin);
+}
+
 // ---- gradient norm
 __device__ double block_sum(double v, double* red) {
 #pragma unroll
@@ -186,22 +343,50 @@ __device__ double block_sum(double v, double* red) {
   return total;
 }
 
+// A block takes chunks blockIdx.x, + gridDim.x, ...; the vectors of a tensor
+// start at its first 32-byte boundary, and the values before it go with the
+// first chunk.
 template <int kCapacity>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ List<kCapacity> list,
                                                            double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
-  float s = 0.0f;
+  constexpr int kPer = kNormChunkValues / (kThreads * 8);
+  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   for (int chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
     const int which = tensor_of(list, chunk);
     const Tensor& t = list.t[which];
-    const int64_t begin = static_cast<int64_t>(chunk - list.first[which]) * kChunkValues;
-    const int64_t end = begin + kChunkValues < t.n ? begin + kChunkValues : t.n;
-    for (int64_t j = begin + threadIdx.x; j < end; j += kThreads) {
-      const float g = load_any(t.grad, t.grad_type, j);
-      s += g * g;
+    const int esize = t.grad_type == MOE_F32 ? 4 : 2;
+    const int64_t head = static_cast<int64_t>((32 - (reinterpret_cast<uintptr_t>(t.grad) & 31)) & 31) / esize;
+    const int64_t begin = head + static_cast<int64_t>(chunk - list.first[which]) * kNormChunkValues;
+    if (chunk == list.first[which])
+      for (int64_t j = threadIdx.x; j < head && j < t.n; j += kThreads) {
+        const float g = load_any(t.grad, t.grad_type, j);
+        s[0] += g * g;
+      }
+    Raw8 raw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t j = begin + (i * kThreads + threadIdx.x) * 8;
+      if (j + 8 <= t.n) load8(t.grad, t.grad_type, j, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t j = begin + (i * kThreads + threadIdx.x) * 8;
+      if (j + 8 <= t.n) {
+        float g[8];
+        values8(raw[i], t.grad_type, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] += g[k] * g[k];
+      } else {
+        for (int64_t k = j; k < t.n; ++k) {
+          const float g = load_any(t.grad, t.grad_type, k);
+          s[0] += g * g;
+        }
+      }
     }
   }
-  const double total = block_sum(s, red);
+  const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+  const double total = block_sum(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
@@ -219,20 +404,27 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict
 }
 
 // ---- lists
+bool all_aligned(const moe_adamw_tensor_t& s) {
+  uintptr_t low = reinterpret_cast<uintptr_t>(s.param) | reinterpret_cast<uintptr_t>(s.master) |
+                  reinterpret_cast<uintptr_t>(s.grad) | reinterpret_cast<uintptr_t>(s.m) |
+                  reinterpret_cast<uintptr_t>(s.v);
+  return low % 32 == 0;
+}
+
 template <int kCapacity>
-int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, int* at) {
+int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, int chunk_values, int* at) {
   list.count = 0;
   int64_t chunks = 0;
   while (*at < n_tensors && list.count < kCapacity) {
     const moe_adamw_tensor_t& s = tensors[*at];
-    const int64_t more = (s.n + kChunkValues - 1) / kChunkValues;
+    const int64_t more = (s.n + chunk_values - 1) / chunk_values;
     if (chunks + more > INT32_MAX) break;
     ++*at;
     if (s.n == 0) continue;
     list.first[list.count] = static_cast<int>(chunks);
     list.t[list.count++] = Tensor{s.param, s.master, s.grad, s.m, s.v, s.m_scale, s.v_scale, s.n, s.decay,
                                   static_cast<uint8_t>(s.param_type), static_cast<uint8_t>(s.grad_type),
-                                  static_cast<uint8_t>(s.state_bits == 8), 0};
+                                  static_cast<uint8_t>(s.state_bits == 8), static_cast<uint8_t>(all_aligned(s))};
     chunks += more;
   }
   list.chunks = static_cast<int>(chunks);
@@ -247,7 +439,7 @@ cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const mo
   list.hyper_dev = hyper_dev;
   list.grad_scale = grad_scale;
   for (int at = 0; at < n_tensors;) {
-    if (fill(list, tensors, n_tensors, &at) == 0) continue;
+    if (fill(list, tensors, n_tensors, kChunkValues, &at) == 0) continue;
     adamw_kernel<kCapacity><<<list.chunks, kThreads, 0, stream>>>(list);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
@@ -265,7 +457,7 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
   if (most < 1) return cudaErrorInvalidValue;
   int blocks = 0;
   for (int at = 0; at < n_tensors;) {
-    const int chunks = fill(list, tensors, n_tensors, &at);
+    const int chunks = fill(list, tensors, n_tensors, kNormChunkValues, &at);
     if (chunks == 0) continue;
     const int grid = chunks < most ? chunks : most;
     if (blocks + grid > kGradNormMaxBlocks) return cudaErrorInvalidValue;

@@ -11,19 +11,29 @@
 // read once, its maximum, exponential sum and dot product with the shares
 // are reduced inside the lanes that hold it, and its gradient written.
 //
-// A group of `tpr` lanes (a power of two, up to a warp) holds a row, value
-// lane + i * tpr in lane `lane`.
+// A group of `tpr` lanes (a power of two, up to a warp) holds a row: vectors
+// of four values lane, lane + tpr, ... where rows and E allow 16-byte
+// accesses, else single values.  Warps walk over the rows with the next
+// row's loads in flight.
+//
+// The mask is counted by a kernel of its own first: every block needs N, and
+// each counting for itself (in the first version) cost more than the losses
+// (65,536 tokens: 349 us in all).
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCountBlocks = 64;
 
 struct Args {
   RouterLoss a;
+  const int32_t* kept;  // [kCountBlocks] tokens kept, by the counting kernel; null without a mask
+  double* partial;      // [blocks][2]
   int tpr;
 };
 
@@ -32,62 +42,108 @@ __device__ __forceinline__ float group_max(float v, int width) {
   return v;
 }
 
-// Sum over the block in a fixed order, in thread 0.
-__device__ double block_sum(double v, double* red) {
+// Sum over the block in a fixed order, in every thread.
+template <typename T>
+__device__ T block_sum(T v, T* red) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double total = 0.0;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) total += red[i];
+  T total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) total += red[i];
   __syncthreads();
   return total;
 }
 
-template <int kValues>
+__global__ void __launch_bounds__(kThreads) count_kernel(const uint8_t* __restrict__ mask, int64_t T,
+                                                         int32_t* __restrict__ kept) {
+  __shared__ int red[kThreads / 32];
+  let_next_start();
+  int n = 0;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  // bytes up to a 16-byte boundary, whole vectors, the rest
+  int64_t head = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(mask) & 15)) & 15);
+  if (head > T) head = T;
+  const int64_t vectors = (T - head) / 16;
+  for (int64_t i = first; i < vectors; i += stride) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(mask + head) + i);
+    // a byte of __vcmpgtu4 is 255 where the mask's byte is above 0
+    n += (__popc(__vcmpgtu4(u.x, 0)) + __popc(__vcmpgtu4(u.y, 0)) + __popc(__vcmpgtu4(u.z, 0)) +
+          __popc(__vcmpgtu4(u.w, 0))) >> 3;
+  }
+  const int64_t tail = head + vectors * 16;
+  if (first < head) n += mask[first] != 0;
+  if (tail + first < T) n += mask[tail + first] != 0;
+  n = block_sum(n, red);
+  if (threadIdx.x == 0) kept[blockIdx.x] = n;
+}
+
+// Column of value i of a lane.
+template <bool kVec>
+__device__ __forceinline__ int column(int i, int lane, int tpr) {
+  return kVec ? ((i >> 2) * tpr + lane) * 4 + (i & 3) : i * tpr + lane;
+}
+
+template <int kValues, bool kVec>
+__device__ __forceinline__ void load_row(const float* row, bool live, float fill, int E, int lane, int tpr,
+                                         float (&v)[kValues]) {
+#pragma unroll
+  for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
+    const int e = column<kVec>(i, lane, tpr);
+    if (kVec) {
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (live && e < E) q = *reinterpret_cast<const float4*>(row + e);
+      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    } else {
+      v[i] = live && e < E ? row[e] : fill;
+    }
+  }
+}
+
+template <int kValues, bool kVec>
 __global__ void __launch_bounds__(kThreads) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
   const int tpr = args.tpr, E = a.E;
+  __shared__ int64_t red_i[kThreads / 32];
   __shared__ double red[kThreads / 32];
-  __shared__ double shared_n, shared_counts;
-  // N and the total of the counts: every block adds them up for itself
-  double kept = 0.0, counted = 0.0;
-  if (a.mask)
-    for (int64_t t = threadIdx.x; t < a.T; t += kThreads) kept += a.mask[t] != 0 ? 1.0 : 0.0;
-  for (int e = threadIdx.x; e < E; e += kThreads) counted += static_cast<double>(a.counts[e]);
-  kept = block_sum(kept, red);
-  counted = block_sum(counted, red);
-  if (threadIdx.x == 0) {
-    shared_n = a.mask ? kept : static_cast<double>(a.T);
-    shared_counts = counted;
-  }
-  __syncthreads();
-  const float inv_n = shared_n > 0.0 ? static_cast<float>(1.0 / shared_n) : 0.0f;
+  let_next_start();
   const int lane = threadIdx.x % tpr;
+  int64_t counted = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) counted += a.counts[e];
+  counted = block_sum(counted, red_i);
   float share[kValues];
 #pragma unroll
   for (int i = 0; i < kValues; ++i) {
-    const int e = lane + i * tpr;
-    share[i] = e < E && shared_counts > 0.0 ? static_cast<float>(a.counts[e] / shared_counts) : 0.0f;
+    const int e = column<kVec>(i, lane, tpr);
+    share[i] = e < E && counted > 0 ? static_cast<float>(a.counts[e] / static_cast<double>(counted)) : 0.0f;
   }
   const float cb = a.balance_coef * static_cast<float>(E), cz = 2.0f * a.z_coef;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr;
+  const int64_t rounds = (a.T - static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + step - 1) / step;
+  bool live = t < a.T && (!a.mask || a.mask[t] != 0);
+  float l[kValues], before[kValues];
+  load_row<kValues, kVec>(a.logits + t * E, live, -INFINITY, E, lane, tpr, l);
+  if (a.d_in) load_row<kValues, kVec>(a.d_in + t * E, live, 0.0f, E, lane, tpr, before);
+  int64_t n = a.T;
+  if (args.kept) {
+    wait_for_previous();
+    n = 0;
+    for (int i = 0; i < kCountBlocks; ++i) n += args.kept[i];
+  }
+  const float inv_n = n > 0 ? static_cast<float>(1.0 / static_cast<double>(n)) : 0.0f;
   float sum_s = 0.0f, sum_z = 0.0f;
-  const int groups = kThreads / tpr;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * groups; t0 < a.T;
-       t0 += static_cast<int64_t>(gridDim.x) * groups) {
-    const int64_t t = t0 + threadIdx.x / tpr;
-    const bool row = t < a.T;
-    const bool live = row && (!a.mask || a.mask[t] != 0);
-    const int64_t base = t * E;
-    float l[kValues];
+  for (int64_t round = 0; round < rounds; ++round, t += step) {
+    // the next row, before this one is used
+    const int64_t next = t + step;
+    const bool next_live = next < a.T && (!a.mask || a.mask[next] != 0);
+    float next_l[kValues], next_before[kValues];
+    load_row<kValues, kVec>(a.logits + next * E, next_live, -INFINITY, E, lane, tpr, next_l);
+    if (a.d_in) load_row<kValues, kVec>(a.d_in + next * E, next_live, 0.0f, E, lane, tpr, next_before);
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      const int e = lane + i * tpr;
-      l[i] = live && e < E ? __ldg(a.logits + base + e) : -INFINITY;
-      top = fmaxf(top, l[i]);
-    }
+    for (int i = 0; i < kValues; ++i) top = fmaxf(top, l[i]);
     top = group_max(top, tpr);
     const bool empty = top == -INFINITY;  // masked, or every logit is -infinity
     float z = 0.0f, dot = 0.0f;
@@ -104,36 +160,52 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const Args args) {
     const float inv_z = empty && z == 0.0f ? 0.0f : 1.0f / z;
     const float s = dot * inv_z;
     const float lse = empty && z == 0.0f ? 0.0f : top + logf(z);
-    if (lane == 0) {
-      sum_s += s;
-      sum_z += lse * lse;
+    sum_s += s;
+    sum_z += lse * lse;
+    // a masked row of an accumulated gradient is left as it is
+    if (t < a.T && (live || !a.d_in || a.d_in != a.d_logits)) {
+      const float zl = cz * lse, scale = inv_z * inv_n;
+      float* row = a.d_logits + t * E;
+#pragma unroll
+      for (int i = 0; i < kValues; ++i) {
+        l[i] = live ? l[i] * scale * (cb * (share[i] - s) + zl) : 0.0f;
+        if (a.d_in) {
+          const int e = column<kVec>(i, lane, tpr);
+          if (!live && e < E) before[i] = a.d_in[t * E + e];
+          l[i] += before[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
+        const int e = column<kVec>(i, lane, tpr);
+        if (e >= E) continue;
+        if (kVec) *reinterpret_cast<float4*>(row + e) = make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
+        else row[e] = l[i];
+      }
     }
-    if (!row) continue;
-    const float zl = cz * lse, scale = inv_z * inv_n;
+    live = next_live;
 #pragma unroll
     for (int i = 0; i < kValues; ++i) {
-      const int e = lane + i * tpr;
-      if (e >= E) continue;
-      float d = l[i] * scale * (cb * (share[i] - s) + zl);
-      if (!live) d = 0.0f;
-      if (a.d_in) d += a.d_in[base + e];
-      a.d_logits[base + e] = d;
+      l[i] = next_l[i];
+      before[i] = next_before[i];
     }
   }
-  const double s = block_sum(sum_s, red), z = block_sum(sum_z, red);
+  // every lane of a group carries the row's sums: one of them counts
+  const double s = block_sum(lane == 0 ? static_cast<double>(sum_s) : 0.0, red);
+  const double z = block_sum(lane == 0 ? static_cast<double>(sum_z) : 0.0, red);
   if (threadIdx.x == 0) {
-    const double inv = shared_n > 0.0 ? 1.0 / shared_n : 0.0;
-    double* out = reinterpret_cast<double*>(a.partial) + 2 * blockIdx.x;
-    out[0] = s * E * inv;
-    out[1] = z * inv;
+    const double inv = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+    args.partial[2 * blockIdx.x] = s * E * inv;
+    args.partial[2 * blockIdx.x + 1] = z * inv;
   }
 }
 
-__global__ void __launch_bounds__(256) finish_kernel(const double* __restrict__ partial, int blocks,
-                                                     float* __restrict__ losses) {
-  __shared__ double red[8];
+__global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restrict__ partial, int blocks,
+                                                          float* __restrict__ losses) {
+  __shared__ double red[kThreads / 32];
+  wait_for_previous();
   double s = 0.0, z = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += 256) {
+  for (int b = threadIdx.x; b < blocks; b += kThreads) {
     s += partial[2 * b];
     z += partial[2 * b + 1];
   }
@@ -145,27 +217,51 @@ __global__ void __launch_bounds__(256) finish_kernel(const double* __restrict__ 
   }
 }
 
+// After the counting kernel the losses may start early (they wait for its
+// result); without it they follow the caller's work as any launch does.
+template <int kValues, bool kVec>
+cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
+  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec>, grid, kThreads, 0, stream, args);
+  loss_kernel<kValues, kVec><<<grid, kThreads, 0, stream>>>(args);
+  return cudaGetLastError();
+}
+
+template <bool kVec>
+cudaError_t launch_losses(const Args& args, int values, int grid, cudaStream_t stream) {
+  if (values <= 4) return launch_one<4, kVec>(args, grid, stream);
+  if (values <= 8) return launch_one<8, kVec>(args, grid, stream);
+  if (values <= 12) return launch_one<12, kVec>(args, grid, stream);
+  if (values <= 16) return launch_one<16, kVec>(args, grid, stream);
+  return launch_one<32, kVec>(args, grid, stream);
+}
+
+constexpr size_t kPartialBytes = kRouterLossMaxBlocks * 2 * sizeof(double);
+
 }  // namespace
 
-size_t router_loss_workspace_bytes() { return align_up(kRouterLossMaxBlocks * 2 * sizeof(double)); }
+size_t router_loss_workspace_bytes() { return align_up(kPartialBytes + kCountBlocks * sizeof(int32_t)); }
 
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream) {
-  Args args{a, 1};
-  while (args.tpr < 32 && args.tpr * 4 < a.E) args.tpr *= 2;
-  const int values = (a.E + args.tpr - 1) / args.tpr;
+  auto* kept = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + kPartialBytes);
+  Args args{a, a.mask ? kept : nullptr, static_cast<double*>(a.workspace), 1};
+  const uintptr_t low = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_in) |
+                        reinterpret_cast<uintptr_t>(a.d_logits);
+  const bool vec = a.E % 4 == 0 && low % 16 == 0;
+  const int units = vec ? a.E / 4 : a.E, per = vec ? 1 : 4;
+  while (args.tpr < 32 && args.tpr * per < units) args.tpr *= 2;
+  const int values = (units + args.tpr - 1) / args.tpr * (vec ? 4 : 1);
   const int groups = kThreads / args.tpr;
   const int64_t want = (a.T + groups - 1) / groups;
-  const int64_t most = num_sms * 6 < kRouterLossMaxBlocks ? num_sms * 6 : kRouterLossMaxBlocks;
+  const int64_t most = num_sms * 4 < kRouterLossMaxBlocks ? num_sms * 4 : kRouterLossMaxBlocks;
   const int grid = static_cast<int>(want < most ? want : most);
-  if (values <= 4) loss_kernel<4><<<grid, kThreads, 0, stream>>>(args);
-  else if (values <= 8) loss_kernel<8><<<grid, kThreads, 0, stream>>>(args);
-  else if (values <= 12) loss_kernel<12><<<grid, kThreads, 0, stream>>>(args);
-  else if (values <= 16) loss_kernel<16><<<grid, kThreads, 0, stream>>>(args);
-  else loss_kernel<32><<<grid, kThreads, 0, stream>>>(args);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err;
+  if (a.mask) {
+    count_kernel<<<kCountBlocks, kThreads, 0, stream>>>(a.mask, a.T, kept);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  err = vec ? launch_losses<true>(args, values, grid, stream) : launch_losses<false>(args, values, grid, stream);
   if (err != cudaSuccess) return err;
-  finish_kernel<<<1, 256, 0, stream>>>(reinterpret_cast<const double*>(a.partial), grid, a.losses);
-  return cudaGetLastError();
+  return launch_dependent(finish_kernel, 1, kThreads, 0, stream, args.partial, grid, a.losses);
 }
 
 }  // namespace moe
