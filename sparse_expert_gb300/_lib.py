@@ -115,7 +115,7 @@ SIGNATURES = {
                                      _P]),
     "moe_router_loss_workspace_bytes": (_SZ, []),
     "moe_router_loss": (_S, [_P, _P, _P, _I64, _I32, _F, _F, _P, _P, _P, _P, _SZ, _P]),
-    "moe_adamw_hyper": (_S, [_D, _D, _D, _D, _D, _I64, ctypes.POINTER(AdamWHyper)]),
+    "moe_adamw_hyper": (_S, [_D, _D, _D, _D, _D, _I64, _P]),
     "moe_adamw_step": (_S, [_P, _I32, _P, _P, _P, _P]),
     "moe_grad_norm_workspace_bytes": (_SZ, []),
     "moe_grad_norm": (_S, [_P, _I32, _F, _P, _P, _SZ, _P]),
@@ -689,75 +689,88 @@ def moe_dispatch_noalloc_status(stream=None) -> int:
 
 
 # ------------------------------------------- the training step around the layer
+#
+# These calls can be as short as their launch (a few microseconds), so their
+# checks take the cheap accessors and look closer only where one fails.  With
+# a stream argument everything runs under that stream, allocations included:
+# memory taken from the current stream's pool could be handed out again there
+# while the other stream's kernel still uses it.
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # moe_dtype_t
-
-
-def _raw_stream(stream):
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # cudaStream_t of the current stream of a device index
 
 
 def _rows(t, name, shape=None, dtype=None):
     """Checks a [T, d] tensor of rows (unit stride along d) and returns its row stride."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _DTYPES):
         raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be {'[T, d]' if shape is None else list(shape)}, got {list(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    stride = t.stride()
+    if stride[1] != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.stride(0)
+    return stride[0]
 
 
-def _norm_params(d, dtype, *params):
-    """Checks weight and bias (each [d] or None, of one type) and returns that type."""
-    wdt = None
-    for t, name in params:
-        if t is None:
-            continue
-        if t.dtype != torch.float32 and t.dtype != dtype:
-            raise TypeError(f"{name} must be float32 or {dtype}, got {t.dtype}")
-        if wdt is not None and t.dtype != wdt:
-            raise TypeError("weight and bias must have one type")
-        wdt = t.dtype
-        if t.shape != (d,):
-            raise ValueError(f"{name} must be [{d}], got {list(t.shape)}")
+def _norm_param(t, name, d, dtype):
+    """Checks a weight or bias [d] and returns its moe_dtype_t."""
+    wdt = t.dtype
+    if wdt is not dtype and wdt is not torch.float32:
+        raise TypeError(f"{name} must be float32 or {dtype}, got {wdt}")
+    if t.shape != (d,):
+        raise ValueError(f"{name} must be [{d}], got {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
         _contig(t, wdt, name)
-    return dtype if wdt is None else wdt
+    return _DTYPES[wdt]
+
+
+def _out(t, shape, dtype, name):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _contig(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
 
 
 def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, stats=None, z=None, stream=None):
     """(y [T,d], stats [2,T]) of the rows of x [T,d] (any row stride), or
     (y, stats, z) with a residual: z = x + residual, y = layer norm of z.
     stats (mean, then reciprocal standard deviation) is what the backward reads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_layer_norm(x, weight, bias, eps, residual, out, stats, z)
     x_stride = _rows(x, "x")
-    T, d = x.shape
-    dt = x.dtype
-    wdt = _norm_params(d, dt, (weight, "weight"), (bias, "bias"))
+    shape, dt = x.shape, x.dtype
+    T, d = shape
+    code = wcode = _DTYPES[dt]
+    w_ptr = b_ptr = r_ptr = z_ptr = None
     r_stride = 0
+    if weight is not None:
+        wcode = _norm_param(weight, "weight", d, dt)
+        w_ptr = weight.data_ptr()
+    if bias is not None:
+        bcode = _norm_param(bias, "bias", d, dt)
+        if weight is not None and bcode != wcode:
+            raise TypeError("weight and bias must have one type")
+        wcode, b_ptr = bcode, bias.data_ptr()
+    dev = x.device
     if residual is not None:
-        r_stride = _rows(residual, "residual", x.shape, dt)
-        z = torch.empty(T, d, dtype=dt, device=x.device) if z is None else _out(z, x.shape, dt, "z")
+        r_stride, r_ptr = _rows(residual, "residual", shape, dt), residual.data_ptr()
+        z = torch.empty(shape, dtype=dt, device=dev) if z is None else _out(z, shape, dt, "z")
+        z_ptr = z.data_ptr()
     elif z is not None:
         raise ValueError("z is written with a residual only")
-    out = torch.empty(T, d, dtype=dt, device=x.device) if out is None else _out(out, x.shape, dt, "out")
+    out = torch.empty(shape, dtype=dt, device=dev) if out is None else _out(out, shape, dt, "out")
     if stats is None:
-        stats = torch.empty(2, T, dtype=torch.float32, device=x.device)
+        stats = torch.empty((2, T), dtype=torch.float32, device=dev)
     else:
         _out(stats, (2, T), torch.float32, "stats")
-    _check(lib.moe_layer_norm(x.data_ptr(), x_stride, residual.data_ptr() if residual is not None else None, r_stride,
-                              weight.data_ptr() if weight is not None else None,
-                              bias.data_ptr() if bias is not None else None, T, d, _DTYPES[dt], _DTYPES[wdt], eps,
-                              out.data_ptr(), z.data_ptr() if z is not None else None, stats.data_ptr(),
-                              _raw_stream(stream)), "moe_layer_norm")
+    status = lib.moe_layer_norm(x.data_ptr(), x_stride, r_ptr, r_stride, w_ptr, b_ptr, T, d, code, wcode, eps,
+                                out.data_ptr(), z_ptr, stats.data_ptr(), _raw_stream(dev.index))
+    if status:
+        _check(status, "moe_layer_norm")
     return (out, stats) if residual is None else (out, stats, z)
-
-
-def _out(t, shape, dtype, name):
-    _contig(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
 
 
 def moe_layer_norm_backward_workspace_bytes(T, d) -> int:
@@ -769,32 +782,53 @@ def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads
     z: its z, or its x without a residual; dz: the gradient that reaches z by
     the residual path, added to dx.  dweight is None without a weight, dbias
     with bias=False.  grads: such a dict to write into."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_layer_norm_backward(dy, z, stats, weight, bias, dz, grads, workspace)
     dy_stride = _rows(dy, "dy")
-    T, d = dy.shape
-    dt, dev = dy.dtype, dy.device
-    z_stride = _rows(z, "z", dy.shape, dt)
-    wdt = _norm_params(d, dt, (weight, "weight"))
+    shape, dt, dev = dy.shape, dy.dtype, dy.device
+    T, d = shape
+    z_stride = _rows(z, "z", shape, dt)
+    code = wcode = _DTYPES[dt]
+    w_ptr = dz_ptr = dw_ptr = db_ptr = None
+    if weight is not None:
+        wcode = _norm_param(weight, "weight", d, dt)
+        w_ptr = weight.data_ptr()
     _out(stats, (2, T), torch.float32, "stats")
-    dz_stride = _rows(dz, "dz", dy.shape, dt) if dz is not None else 0
+    dz_stride = 0
+    if dz is not None:
+        dz_stride, dz_ptr = _rows(dz, "dz", shape, dt), dz.data_ptr()
     if grads is None:
-        sums = torch.empty(2, d, dtype=torch.float32, device=dev)
-        grads = dict(dx=torch.empty(T, d, dtype=dt, device=dev), dweight=sums[0] if weight is not None else None,
-                     dbias=sums[1] if bias else None)
+        grads = dict(dx=torch.empty(shape, dtype=dt, device=dev),
+                     dweight=torch.empty(d, dtype=torch.float32, device=dev) if weight is not None else None,
+                     dbias=torch.empty(d, dtype=torch.float32, device=dev) if bias else None)
+        dw, db = grads["dweight"], grads["dbias"]
     else:
-        _out(grads["dx"], dy.shape, dt, "dx")
-        for name in ("dweight", "dbias"):
-            if grads[name] is not None:
-                _out(grads[name], (d,), torch.float32, name)
-    dw, db = grads["dweight"], grads["dbias"]
+        dw, db = grads["dweight"], grads["dbias"]
+        _out(grads["dx"], shape, dt, "dx")
+        if dw is not None:
+            _out(dw, (d,), torch.float32, "dweight")
+        if db is not None:
+            _out(db, (d,), torch.float32, "dbias")
+    if dw is not None:
+        dw_ptr = dw.data_ptr()
+    if db is not None:
+        db_ptr = db.data_ptr()
     if workspace is None:
-        workspace = torch.empty(lib.moe_layer_norm_backward_workspace_bytes(T, d), dtype=torch.uint8, device=dev)
-    _check(lib.moe_layer_norm_backward(dy.data_ptr(), dy_stride, z.data_ptr(), z_stride, stats.data_ptr(),
-                                       weight.data_ptr() if weight is not None else None,
-                                       dz.data_ptr() if dz is not None else None, dz_stride, T, d, _DTYPES[dt],
-                                       _DTYPES[wdt], grads["dx"].data_ptr(), dw.data_ptr() if dw is not None else None,
-                                       db.data_ptr() if db is not None else None, workspace.data_ptr(),
-                                       workspace.numel(), _raw_stream(stream)), "moe_layer_norm_backward")
+        size = lib.moe_layer_norm_backward_workspace_bytes(T, d)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel()
+    status = lib.moe_layer_norm_backward(dy.data_ptr(), dy_stride, z.data_ptr(), z_stride, stats.data_ptr(), w_ptr,
+                                         dz_ptr, dz_stride, T, d, code, wcode, grads["dx"].data_ptr(), dw_ptr, db_ptr,
+                                         workspace.data_ptr(), size, _raw_stream(dev.index))
+    if status:
+        _check(status, "moe_layer_norm_backward")
     return grads
+
+
+_ROUTER_LOSS_WORKSPACE = lib.moe_router_loss_workspace_bytes()
+_GRAD_NORM_WORKSPACE = lib.moe_grad_norm_workspace_bytes()
 
 
 def moe_router_loss(logits, counts, balance_coef=0.01, z_coef=0.001, mask=None, accumulate=None, out=None, losses=None,
@@ -805,33 +839,40 @@ def moe_router_loss(logits, counts, balance_coef=0.01, z_coef=0.001, mask=None, 
     counts [E] int32: the tokens each expert received; mask [T] bool: tokens
     to count; accumulate: a [T,E] gradient that this one is added to, in
     place (moe_backward's d_logits)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_router_loss(logits, counts, balance_coef, z_coef, mask, accumulate, out, losses, workspace)
     _contig(logits, torch.float32, "logits")
-    T, E = logits.shape
-    dev = logits.device
+    shape, dev = logits.shape, logits.device
+    T, E = shape
     _out(counts, (E,), torch.int32, "counts")
+    m_ptr = a_ptr = None
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
-        _out(mask, (T,), mask.dtype, "mask")
+        m_ptr = _out(mask, (T,), mask.dtype, "mask").data_ptr()
     if accumulate is not None:
-        _out(accumulate, logits.shape, torch.float32, "accumulate")
         if out is not None:
             raise ValueError("accumulate is written in place: give it or out")
-        out = accumulate
+        out = _out(accumulate, shape, torch.float32, "accumulate")
+        a_ptr = out.data_ptr()
     elif out is None:
-        out = torch.empty(T, E, dtype=torch.float32, device=dev)
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
-        _out(out, logits.shape, torch.float32, "out")
+        _out(out, shape, torch.float32, "out")
     if losses is None:
         losses = torch.empty(2, dtype=torch.float32, device=dev)
     else:
         _out(losses, (2,), torch.float32, "losses")
     if workspace is None:
-        workspace = torch.empty(lib.moe_router_loss_workspace_bytes(), dtype=torch.uint8, device=dev)
-    _check(lib.moe_router_loss(logits.data_ptr(), counts.data_ptr(), mask.data_ptr() if mask is not None else None, T,
-                               E, balance_coef, z_coef, accumulate.data_ptr() if accumulate is not None else None,
-                               out.data_ptr(), losses.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                               _raw_stream(stream)), "moe_router_loss")
+        size = _ROUTER_LOSS_WORKSPACE
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel()
+    status = lib.moe_router_loss(logits.data_ptr(), counts.data_ptr(), m_ptr, T, E, balance_coef, z_coef, a_ptr,
+                                 out.data_ptr(), losses.data_ptr(), workspace.data_ptr(), size, _raw_stream(dev.index))
+    if status:
+        _check(status, "moe_router_loss")
     return losses, out
 
 
@@ -841,7 +882,9 @@ class TensorList:
     so that the records' pointers stay valid."""
 
     def __init__(self, records, tensors, device, has_states):
-        self.records, self.tensors, self.device, self.has_states = records, tensors, device, has_states
+        self.records, self.tensors, self.has_states = records, tensors, has_states
+        self.device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.address, self.count = ctypes.addressof(records), len(records)
 
     def __len__(self):
         return len(self.records)
@@ -928,17 +971,25 @@ def moe_grad_norm(tensors, max_norm=float("inf"), out=None, workspace=None, stre
     moe_tensor_list or a sequence of tensors; factor = max_norm / norm where
     the norm is larger, else 1 (NaN for a norm that is not finite): the `clip`
     argument of moe_adamw_step."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_grad_norm(tensors, max_norm, out, workspace)
     if not isinstance(tensors, TensorList):
         tensors = moe_tensor_list(tensors)
-    device = tensors.device if tensors.device is not None else torch.device("cuda", torch.cuda.current_device())
+    dev = tensors.device
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=device)
+        out = torch.empty(2, dtype=torch.float32, device=dev)
     else:
         _out(out, (2,), torch.float32, "out")
     if workspace is None:
-        workspace = torch.empty(lib.moe_grad_norm_workspace_bytes(), dtype=torch.uint8, device=device)
-    _check(lib.moe_grad_norm(tensors.records, len(tensors.records), max_norm, out.data_ptr(), workspace.data_ptr(),
-                             workspace.numel(), _raw_stream(stream)), "moe_grad_norm")
+        size = _GRAD_NORM_WORKSPACE
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        size = workspace.numel()
+    status = lib.moe_grad_norm(tensors.address, tensors.count, max_norm, out.data_ptr(), workspace.data_ptr(), size,
+                               _raw_stream(dev.index))
+    if status:
+        _check(status, "moe_grad_norm")
     return out
 
 
@@ -970,7 +1021,11 @@ def moe_adamw_step(plan, lr=None, step=None, betas=(0.9, 0.95), eps=1e-8, weight
         if lr is None or step is None:
             raise ValueError("lr and step are needed without hyper")
         h = AdamWHyper()
-        _check(lib.moe_adamw_hyper(lr, betas[0], betas[1], eps, weight_decay, step, ctypes.byref(h)), "moe_adamw_hyper")
         host, dev = ctypes.addressof(h), None
-    _check(lib.moe_adamw_step(plan.records, len(plan.records), host, dev, scale, _raw_stream(stream)),
-           "moe_adamw_step")
+        status = lib.moe_adamw_hyper(lr, betas[0], betas[1], eps, weight_decay, step, host)
+        if status:
+            _check(status, "moe_adamw_hyper")
+    status = lib.moe_adamw_step(plan.address, plan.count, host, dev, scale,
+                                _raw_stream(plan.device.index) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "moe_adamw_step")

@@ -113,7 +113,7 @@ moe_status_t moe_layer_norm(const void* x, int64_t x_stride, const void* residua
   if ((s = device_info(&dev)) != MOE_OK) return s;
   const cudaError_t e = launch_layer_norm(NormForward{x, x_stride, residual, residual_stride, weight, bias, T, d, dtype,
                                                       weight_dtype, eps, y, z, stats},
-                                          static_cast<cudaStream_t>(stream));
+                                          dev.num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "layer norm launch");
 }
 

@@ -251,7 +251,7 @@ struct NormForward {
   void* z;       // with a residual: round(x + residual)
   float* stats;  // [2][T]: mean, reciprocal standard deviation
 };
-cudaError_t launch_layer_norm(const NormForward& f, cudaStream_t stream);
+cudaError_t launch_layer_norm(const NormForward& f, int num_sms, cudaStream_t stream);
 struct NormBackward {
   const void* dy;
   int64_t dy_stride;
