@@ -77,6 +77,73 @@ __device__ __forceinline__ uint4 pack_chunk(const float* v) {
   return make_uint4(Word<T>::pack(v), Word<T>::pack(v + k), Word<T>::pack(v + 2 * k), Word<T>::pack(v + 3 * k));
 }
 
+// Two fp32 operations in one instruction, each rounded on its own.
+__device__ __forceinline__ uint64_t pair_bits(float2 v) {
+  return static_cast<uint64_t>(__float_as_uint(v.x)) | static_cast<uint64_t>(__float_as_uint(v.y)) << 32;
+}
+__device__ __forceinline__ float2 bits_pair(uint64_t u) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(u)), __uint_as_float(static_cast<uint32_t>(u >> 32)));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return bits_pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return bits_pair(r);
+}
+
+// A chunk as pairs, and back.
+template <typename T>
+constexpr int kPairs = kChunk<T> / 2;
+
+template <typename T>
+__device__ __forceinline__ void unpack_pairs(const uint4& u, float2* v) {
+  float f[kChunk<T>];
+  unpack_chunk<T>(u, f);
+#pragma unroll
+  for (int i = 0; i < kPairs<T>; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const float2* v) {
+  float f[kChunk<T>];
+#pragma unroll
+  for (int i = 0; i < kPairs<T>; ++i) f[2 * i] = v[i].x, f[2 * i + 1] = v[i].y;
+  return pack_chunk<T>(f);
+}
+
+// The chunk's sums, each rounded to the type: for the 16-bit types the fp32
+// sum of two of their values rounds to the same value (24 >= 2 * 11 + 2).
+template <typename T>
+__device__ __forceinline__ uint32_t add_word(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t add_word<float>(uint32_t a, uint32_t b) {
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+template <>
+__device__ __forceinline__ uint32_t add_word<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t add_word<__half>(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2_rn(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint4 add_chunks(const uint4& a, const uint4& b) {
+  return make_uint4(add_word<T>(a.x, b.x), add_word<T>(a.y, b.y), add_word<T>(a.z, b.z), add_word<T>(a.w, b.w));
+}
+
 // Sum over the aligned group of `width` (a power of two up to 32) lanes that
 // the calling lane belongs to, the same value on each.
 __device__ __forceinline__ float group_sum(float v, int width) {

@@ -9,16 +9,20 @@
 // Both directions are bound by memory: every row is read once and written
 // once.  A row belongs to a group of `tpr` threads (a power of two), and
 // groups walk over the rows.  Three forms, by what the rows allow:
-//   - 16-byte chunks (every row, weight and output at a 16-byte boundary, d
-//     a whole number of chunks, at most 3 chunks a thread of 512): thread i of
-//     a group owns chunks i, i + tpr, ...; it copies its own chunks of the
-//     coming rows into its own slots of shared memory asynchronously, several
-//     rows ahead, and reads only those slots, so the loads of the next rows
-//     cover the reductions of this one without a barrier or a register.
-//     Weight, bias and the column sums of the backward stay in registers for
-//     all of a thread's rows.
-//   - single values (any alignment): thread i owns columns i, i + tpr, ... in
-//     registers, so a warp reads neighbouring values.
+//   - rings of 16-byte chunks, where all operands of a row lie alike within
+//     16 bytes (contiguous tensors of any d do) and 3 chunks a thread of 512
+//     hold a row: thread i of a group owns the aligned chunks i, i + tpr, ...
+//     of its rows; it copies its own chunks of the coming rows into its own
+//     slots of shared memory asynchronously, several rows ahead, and reads
+//     only those slots, so the loads of the next rows cover the reductions of
+//     this one without a barrier or a register.  Weight, bias and the column
+//     sums of the backward stay in registers for all of a thread's rows.
+//     Rows that do not start on a chunk: a group steps over rows in multiples
+//     of a chunk's values, after which a row starts at the same place within
+//     16 bytes, so a thread's columns stay the same; only the first and the
+//     last chunk of such a row are partial, and their other values masked.
+//   - single values (operands that lie differently): thread i owns columns
+//     i, i + tpr, ... in registers, so a warp reads neighbouring values.
 //   - rows longer than that: sweeps over the row, the later ones out of L2.
 // The variance is taken from the deviations from the mean, never as a
 // difference of two sums, so a large common offset costs no digits.  Sums
@@ -97,126 +101,215 @@ __device__ __forceinline__ float param_at(const void* p, bool f32, int j) {
   return f32 ? __ldg(static_cast<const float*>(p) + j) : to_f32(static_cast<const T*>(p)[j]);
 }
 
-// A chunk's worth of weight or bias from column j0 (16-byte aligned).
-template <typename T>
-__device__ __forceinline__ void load_param(const void* p, bool f32, int j0, float* v) {
-  if (f32) {
-#pragma unroll
-    for (int i = 0; i < kChunk<T>; i += 4)
-      *reinterpret_cast<float4*>(v + i) = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + j0 + i));
-  } else {
-    unpack_chunk<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + j0)), v);
-  }
-}
-
 // ---- asynchronous copies of a thread's own chunks
-__device__ __forceinline__ void copy_async(uint4* slot, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(slot)), "l"(src) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t slot, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(src) : "memory");
+}
+// The first `bytes` of the chunk, the rest zero.
+__device__ __forceinline__ void copy_async_part(uint32_t slot, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
+__device__ __forceinline__ uint4 load_slot(uint32_t slot) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot));
+  return u;
+}
+__device__ __forceinline__ void store_slot(uint32_t slot, const uint4& u) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+               : "memory");
+}
 
-// Rows in flight a thread, by its chunks a row: with three operands at most
-// 432 bytes a thread, so 512 threads fill an SM's shared memory.
+// One block of 512 threads an SM.  Rows in flight, by a thread's chunks a
+// row: what the SM's shared memory holds with two operands (forward) or
+// three (backward): at most 432 bytes a thread.
+constexpr int kRingThreads = 512;
+constexpr uint32_t kPitch = kRingThreads * 16;  // bytes between a thread's slots
 template <int kChunks>
-constexpr int kStages = kChunks == 1 ? 8 : kChunks == 2 ? 4 : 3;
-constexpr int kRingThreads = 512;  // resident threads of an SM
+constexpr int kForwardStages = kChunks == 1 ? 8 : kChunks == 2 ? 6 : 4;
+template <int kChunks>
+constexpr int kBackwardStages = kChunks == 1 ? 8 : kChunks == 2 ? 4 : 3;
 
-template <typename T, int kChunks>
-__global__ void __launch_bounds__(kRingThreads) forward_ring_kernel(const ForwardArgs a) {
-  constexpr int N = kChunk<T>, S = kStages<kChunks>;
+// Where a thread's chunks lie, for all of its rows.
+template <typename T, int kChunks, bool kAligned>
+struct Place {
+  static constexpr int N = kChunk<T>;
+  int j0[kChunks];  // first column of each chunk: from -off up, at least d for a chunk beyond the row
+  int d;
+  __device__ __forceinline__ Place(int lane, int tpr, int d_, int off) : d(d_) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) j0[c] = (lane + c * tpr) * N - (kAligned ? 0 : off);
+  }
+  __device__ __forceinline__ bool any(int c) const { return j0[c] < d; }
+  __device__ __forceinline__ bool whole(int c) const { return kAligned || (j0[c] >= 0 && j0[c] + N <= d); }
+  // Copies the chunk.  A partial first chunk is copied whole: its 16 aligned
+  // bytes hold at least one value of the row, so they lie inside the
+  // row's allocation.  A last chunk ends with the row.
+  __device__ __forceinline__ void fetch(uint32_t slot, const T* row, int c) const {
+    if (kAligned || j0[c] + N <= d) copy_async(slot, row + j0[c]);
+    else copy_async_part(slot, row + j0[c], (d - j0[c]) * static_cast<int>(sizeof(T)));
+  }
+  // Values outside the row become `fill`.
+  __device__ __forceinline__ void mask(int c, float2* v, float fill) const {
+    if (whole(c)) return;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const int j = j0[c] + 2 * i;
+      if (j < 0 || j >= d) v[i].x = fill;
+      if (j + 1 < 0 || j + 1 >= d) v[i].y = fill;
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int c, const uint4& u) const {
+    if (whole(c)) {
+      *reinterpret_cast<uint4*>(row + j0[c]) = u;
+      return;
+    }
+    float v[N];
+    unpack_chunk<T>(u, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j0[c] + i >= 0 && j0[c] + i < d) row[j0[c] + i] = from_f32<T>(v[i]);
+  }
+  // The chunk's weights or biases.
+  __device__ __forceinline__ void params(int c, const void* p, bool f32, float missing, float2* v) const {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v[i] = both(missing);
+    if (!p || !any(c)) return;
+    if (kAligned) {
+      if (f32) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 2) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + j0[c] + 2 * i));
+          v[i] = make_float2(q.x, q.y);
+          v[i + 1] = make_float2(q.z, q.w);
+        }
+      } else {
+        unpack_pairs<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + j0[c])), v);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const int j = j0[c] + 2 * i;
+      if (j >= 0 && j < d) v[i].x = param_at<T>(p, f32, j);
+      if (j + 1 >= 0 && j + 1 < d) v[i].y = param_at<T>(p, f32, j + 1);
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ int row_offset(const Row& rows, int64_t t) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(rows.ptr) + t * rows.stride) & 15) /
+                          sizeof(T));
+}
+
+template <typename T, int kChunks, bool kAligned>
+__global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const ForwardArgs a) {
+  constexpr int P = kPairs<T>, S = kForwardStages<kChunks>;
   extern __shared__ uint4 ring[];  // [stage][operand][chunk][thread]
   __shared__ float2 red[2][kMaxWarps];
-  const int groups = blockDim.x / a.tpr, lane = threadIdx.x % a.tpr, d = a.d;
+  const int groups = kRingThreads / a.tpr, lane = threadIdx.x % a.tpr;
   const bool res = a.res.ptr != nullptr;
-  const int per_stage = (res ? 2 : 1) * kChunks;
-  auto slot = [&](int stage, int operand, int c) {
-    return ring + (stage * per_stage + operand * kChunks + c) * blockDim.x + threadIdx.x;
-  };
+  const uint32_t own = smem_addr(ring) + threadIdx.x * 16, stage_bytes = (res ? 2 : 1) * kChunks * kPitch;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups;
   const int64_t rounds = (a.T - first + step - 1) / step;
-  const int64_t t0 = first + threadIdx.x / a.tpr;
-  auto fetch = [&](int64_t round, int stage) {
-    const int64_t t = t0 + round * step;
-    if (t < a.T) {
+  int64_t t = first + threadIdx.x / a.tpr;
+  const Place<T, kChunks, kAligned> at(lane, a.tpr, a.d, kAligned ? 0 : row_offset<T>(a.x, t));
+  const T* x = static_cast<const T*>(a.x.ptr) + t * a.x.stride;
+  const T* r_row = static_cast<const T*>(a.res.ptr) + (res ? t * a.res.stride : 0);
+  int64_t ahead = t;  // the row that x and r_row stand at
+  auto fetch = [&](uint32_t stage) {
+    if (ahead < a.T) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        const int j0 = (lane + c * a.tpr) * N;
-        if (j0 >= d) continue;
-        copy_async(slot(stage, 0, c), static_cast<const T*>(a.x.ptr) + t * a.x.stride + j0);
-        if (res) copy_async(slot(stage, 1, c), static_cast<const T*>(a.res.ptr) + t * a.res.stride + j0);
+        if (!at.any(c)) continue;
+        at.fetch(stage + c * kPitch, x, c);
+        if (res) at.fetch(stage + (kChunks + c) * kPitch, r_row, c);
       }
     }
     copy_commit();
+    ahead += step;
+    x += step * a.x.stride;
+    if (res) r_row += step * a.res.stride;
   };
-  for (int s = 0; s < S - 1; ++s) fetch(s, s);
-  float w[kChunks * N], b[kChunks * N];
+  for (int s = 0; s < S - 1; ++s) fetch(own + s * stage_bytes);
+  float2 w[kChunks * P], b[kChunks * P];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    const int j0 = (lane + c * a.tpr) * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[c * N + i] = 1.0f, b[c * N + i] = 0.0f;
-    if (j0 < d && a.w) load_param<T>(a.w, a.w_f32, j0, w + c * N);
-    if (j0 < d && a.b) load_param<T>(a.b, a.w_f32, j0, b + c * N);
+    at.params(c, a.w, a.w_f32, 1.0f, w + c * P);
+    at.params(c, a.b, a.w_f32, 0.0f, b + c * P);
   }
-  const float inv_d = 1.0f / static_cast<float>(d);
-  int stage = 0;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  uint32_t stage = own, next = own + (S - 1) * stage_bytes;
+  T* y = static_cast<T*>(a.y) + t * a.d;
+  T* z_row = static_cast<T*>(a.z) + t * a.d;
   for (int64_t round = 0; round < rounds; ++round) {
-    fetch(round + S - 1, stage == 0 ? S - 1 : stage - 1);
+    fetch(next);
     copy_wait<S - 1>();
-    const int64_t t = t0 + round * step;
     const bool live = t < a.T;
-    float s = 0.0f;
+    float2 s = both(0.0f);
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int j0 = (lane + c * a.tpr) * N;
-      if (j0 >= d || !live) continue;
-      float v[N], u[N];
-      unpack_chunk<T>(*slot(stage, 0, c), v);
-      if (res) {
-        // the sum is rounded to the rows' type here: it is what the caller
-        // keeps and what the backward normalises again
-        unpack_chunk<T>(*slot(stage, 1, c), u);
+      for (int c = 0; c < kChunks; ++c) {
+        if (!at.any(c)) continue;
+        uint4 u = load_slot(stage + c * kPitch);
+        if (res) {
+          // the sum is rounded to the rows' type here: it is what the caller
+          // keeps and what the backward normalises again
+          u = add_chunks<T>(u, load_slot(stage + (kChunks + c) * kPitch));
+          store_slot(stage + c * kPitch, u);
+          at.store(z_row, c, u);
+        }
+        float2 v[P];
+        unpack_pairs<T>(u, v);
+        at.mask(c, v, 0.0f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += u[i];
-        const uint4 z = pack_chunk<T>(v);
-        *slot(stage, 0, c) = z;
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.z) + t * d + j0) = z;
-        unpack_chunk<T>(z, v);
+        for (int i = 0; i < P; ++i) s = add2(s, v[i]);
+      }
+    }
+    const float mu = group_reduce(s.x + s.y, a.tpr, red[0]) * inv_d;
+    s = both(0.0f);
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        if (!at.any(c)) continue;
+        float2 v[P];
+        unpack_pairs<T>(load_slot(stage + c * kPitch), v);
+        at.mask(c, v, mu);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float2 e = add2(v[i], both(-mu));
+          s = fma2(e, e, s);
+        }
+      }
+    }
+    const float r = 1.0f / sqrtf(group_reduce(s.x + s.y, a.tpr, red[1]) * inv_d + a.eps);
+    if (live) {
+      if (lane == 0) {
+        a.stats[t] = mu;
+        a.stats[a.T + t] = r;
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) s += v[i];
-    }
-    const float mu = group_reduce(s, a.tpr, red[0]) * inv_d;
-    s = 0.0f;
+      for (int c = 0; c < kChunks; ++c) {
+        if (!at.any(c)) continue;
+        float2 v[P];
+        unpack_pairs<T>(load_slot(stage + c * kPitch), v);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      if ((lane + c * a.tpr) * N >= d || !live) continue;
-      float v[N];
-      unpack_chunk<T>(*slot(stage, 0, c), v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s += (v[i] - mu) * (v[i] - mu);
+        for (int i = 0; i < P; ++i)
+          v[i] = fma2(mul2(add2(v[i], both(-mu)), both(r)), w[c * P + i], b[c * P + i]);
+        at.store(y, c, pack_pairs<T>(v));
+      }
     }
-    const float r = 1.0f / sqrtf(group_reduce(s, a.tpr, red[1]) * inv_d + a.eps);
-    if (live && lane == 0) {
-      a.stats[t] = mu;
-      a.stats[a.T + t] = r;
-    }
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int j0 = (lane + c * a.tpr) * N;
-      if (j0 >= d || !live) continue;
-      float v[N];
-      unpack_chunk<T>(*slot(stage, 0, c), v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = (v[i] - mu) * r * w[c * N + i] + b[c * N + i];
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + t * d + j0) = pack_chunk<T>(v);
-    }
-    stage = stage == S - 1 ? 0 : stage + 1;
+    t += step;
+    y += step * a.d;
+    if (res) z_row += step * a.d;
+    next = stage;
+    stage = stage + stage_bytes == own + S * stage_bytes ? own : stage + stage_bytes;
   }
 }
 
@@ -315,137 +408,145 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const ForwardArgs a)
   }
 }
 
-// The block's column sums from its threads': lanes of a warp that own the
-// same columns (tpr below 32) add by a tree, then the warps or groups in
-// order through `shared` (slots x d floats).  column(i): value i's column.
-template <int kValues, typename Column>
-__device__ void write_partial(const BackwardArgs& a, float* sw, float* sb, float* shared, Column column) {
+// The block's column sums from its threads': where the lanes of a warp own
+// the same columns (`same`: tpr below 32, rows that start alike) they add by
+// a tree, then the warps or groups in order through `shared` (slots x d
+// floats).  column(i): value i's column.
+template <int kValues, typename Value, typename Column>
+__device__ __forceinline__ void write_partial(const BackwardArgs& a, int which, bool same, float* shared, Value value,
+                                              Column column) {
   const int tpr = a.tpr, d = a.d;
-  const int slots = tpr < 32 ? blockDim.x >> 5 : blockDim.x / tpr;
-  const int slot = tpr < 32 ? threadIdx.x >> 5 : threadIdx.x / tpr;
-  const bool owner = tpr >= 32 || (threadIdx.x & 31) < tpr;
+  const int width = same && tpr < 32 ? 32 : tpr;  // threads whose sums share a slot
+  const int slots = blockDim.x / width, slot = threadIdx.x / width;
+  const bool owner = threadIdx.x % width < tpr;
+  float* out = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * d;
+  __syncthreads();  // the ring, or the other sum, is done with `shared`
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    if (!(which ? a.want_b : a.want_w)) continue;
-    float* sum = which ? sb : sw;
-    float* out = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * d;
-    if (tpr < 32) {
-#pragma unroll
-      for (int i = 0; i < kValues; ++i)
-        for (int s = 16; s >= tpr; s >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], s);
-    }
-    if (slots == 1) {
-#pragma unroll
-      for (int i = 0; i < kValues; ++i)
-        if (owner && column(i) < d) out[column(i)] = sum[i];
-      continue;
-    }
-    __syncthreads();  // the ring, or the other sum, is done with `shared`
-#pragma unroll
-    for (int i = 0; i < kValues; ++i)
-      if (owner && column(i) < d) shared[slot * d + column(i)] = sum[i];
-    __syncthreads();
-    for (int j = threadIdx.x; j < d; j += blockDim.x) {
-      float s = shared[j];
-      for (int k = 1; k < slots; ++k) s += shared[k * d + j];
-      out[j] = s;
-    }
+  for (int i = 0; i < kValues; ++i) {
+    float s = value(i);
+    for (int k = width >> 1; k >= tpr; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    const int j = column(i);
+    if (owner && j >= 0 && j < d) (slots == 1 ? out : shared + slot * d)[j] = s;
+  }
+  if (slots == 1) return;
+  __syncthreads();
+  for (int j = threadIdx.x; j < d; j += blockDim.x) {
+    float s = shared[j];
+    for (int k = 1; k < slots; ++k) s += shared[k * d + j];
+    out[j] = s;
   }
 }
 
-template <typename T, int kChunks>
-__global__ void __launch_bounds__(kRingThreads) backward_ring_kernel(const BackwardArgs a) {
-  constexpr int N = kChunk<T>, S = kStages<kChunks>;
+template <typename T, int kChunks, bool kAligned>
+__global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const BackwardArgs a) {
+  constexpr int P = kPairs<T>, S = kBackwardStages<kChunks>;
   extern __shared__ uint4 ring[];  // [stage][operand][chunk][thread]
   __shared__ float2 red[2][kMaxWarps];
   let_next_start();
-  const int groups = blockDim.x / a.tpr, lane = threadIdx.x % a.tpr, d = a.d;
+  const int groups = kRingThreads / a.tpr, lane = threadIdx.x % a.tpr;
   const bool add = a.dz.ptr != nullptr;
-  const int per_stage = (add ? 3 : 2) * kChunks;
-  auto slot = [&](int stage, int operand, int c) {
-    return ring + (stage * per_stage + operand * kChunks + c) * blockDim.x + threadIdx.x;
-  };
+  const uint32_t own = smem_addr(ring) + threadIdx.x * 16, stage_bytes = (add ? 3 : 2) * kChunks * kPitch;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * groups;
   const int64_t rounds = (a.T - first + step - 1) / step;
-  const int64_t t0 = first + threadIdx.x / a.tpr;
-  auto fetch = [&](int64_t round, int stage) {
-    const int64_t t = t0 + round * step;
-    if (t < a.T) {
+  int64_t t = first + threadIdx.x / a.tpr;
+  const Place<T, kChunks, kAligned> at(lane, a.tpr, a.d, kAligned ? 0 : row_offset<T>(a.dy, t));
+  const T* dy = static_cast<const T*>(a.dy.ptr) + t * a.dy.stride;
+  const T* z = static_cast<const T*>(a.z.ptr) + t * a.z.stride;
+  const T* dz = static_cast<const T*>(a.dz.ptr) + (add ? t * a.dz.stride : 0);
+  int64_t ahead = t;  // the row that the pointers stand at
+  auto fetch = [&](uint32_t stage) {
+    if (ahead < a.T) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
-        const int j0 = (lane + c * a.tpr) * N;
-        if (j0 >= d) continue;
-        copy_async(slot(stage, 0, c), static_cast<const T*>(a.dy.ptr) + t * a.dy.stride + j0);
-        copy_async(slot(stage, 1, c), static_cast<const T*>(a.z.ptr) + t * a.z.stride + j0);
-        if (add) copy_async(slot(stage, 2, c), static_cast<const T*>(a.dz.ptr) + t * a.dz.stride + j0);
+        if (!at.any(c)) continue;
+        at.fetch(stage + c * kPitch, dy, c);
+        at.fetch(stage + (kChunks + c) * kPitch, z, c);
+        if (add) at.fetch(stage + (2 * kChunks + c) * kPitch, dz, c);
       }
     }
     copy_commit();
+    ahead += step;
+    dy += step * a.dy.stride;
+    z += step * a.z.stride;
+    if (add) dz += step * a.dz.stride;
   };
-  for (int s = 0; s < S - 1; ++s) fetch(s, s);
-  float w[kChunks * N], sw[kChunks * N], sb[kChunks * N];
+  for (int s = 0; s < S - 1; ++s) fetch(own + s * stage_bytes);
+  float2 w[kChunks * P], sw[kChunks * P], sb[kChunks * P];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int j0 = (lane + c * a.tpr) * N;
+  for (int c = 0; c < kChunks; ++c) at.params(c, a.w, a.w_f32, 1.0f, w + c * P);
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[c * N + i] = 1.0f, sw[c * N + i] = sb[c * N + i] = 0.0f;
-    if (j0 < d && a.w) load_param<T>(a.w, a.w_f32, j0, w + c * N);
-  }
-  const float inv_d = 1.0f / static_cast<float>(d);
-  int stage = 0;
+  for (int i = 0; i < kChunks * P; ++i) sw[i] = sb[i] = both(0.0f);
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  uint32_t stage = own, next = own + (S - 1) * stage_bytes;
+  T* dx = static_cast<T*>(a.dx) + t * a.d;
   float mu = 0.0f, r = 0.0f;
-  if (t0 < a.T) mu = __ldg(a.stats + t0), r = __ldg(a.stats + a.T + t0);
+  if (t < a.T) mu = __ldg(a.stats + t), r = __ldg(a.stats + a.T + t);
   for (int64_t round = 0; round < rounds; ++round) {
-    fetch(round + S - 1, stage == 0 ? S - 1 : stage - 1);
-    const int64_t t = t0 + round * step;
-    const bool live = t < a.T;
+    fetch(next);
     float next_mu = 0.0f, next_r = 0.0f;
     if (t + step < a.T) next_mu = __ldg(a.stats + t + step), next_r = __ldg(a.stats + a.T + t + step);
     copy_wait<S - 1>();
-    float2 s = make_float2(0.0f, 0.0f);
+    const bool live = t < a.T;
+    const float2 m2 = both(-mu), r2 = both(r);
+    float2 s1 = both(0.0f), s2 = both(0.0f);
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      if ((lane + c * a.tpr) * N >= d || !live) continue;
-      float g[N], n[N];
-      unpack_chunk<T>(*slot(stage, 0, c), g);
-      unpack_chunk<T>(*slot(stage, 1, c), n);
+      for (int c = 0; c < kChunks; ++c) {
+        if (!at.any(c)) continue;
+        float2 g[P], n[P];
+        unpack_pairs<T>(load_slot(stage + c * kPitch), g);
+        unpack_pairs<T>(load_slot(stage + (kChunks + c) * kPitch), n);
+        at.mask(c, g, 0.0f);
+        at.mask(c, n, mu);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        n[i] = (n[i] - mu) * r;
-        sw[c * N + i] += g[i] * n[i];
-        sb[c * N + i] += g[i];
-        const float gw = g[i] * w[c * N + i];
-        s.x += gw;
-        s.y += gw * n[i];
+        for (int i = 0; i < P; ++i) {
+          n[i] = mul2(add2(n[i], m2), r2);
+          sw[c * P + i] = fma2(g[i], n[i], sw[c * P + i]);
+          sb[c * P + i] = add2(g[i], sb[c * P + i]);
+          g[i] = mul2(g[i], w[c * P + i]);
+          s1 = add2(s1, g[i]);
+          s2 = fma2(g[i], n[i], s2);
+        }
       }
     }
-    s = group_reduce(s, a.tpr, red[round & 1]);
-    s.x *= inv_d;
-    s.y *= inv_d;
+    const float2 sum = group_reduce(make_float2(s1.x + s1.y, s2.x + s2.y), a.tpr, red[round & 1]);
+    if (live) {
+      const float2 m1 = both(-sum.x * inv_d), c2 = both(-sum.y * inv_d);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int j0 = (lane + c * a.tpr) * N;
-      if (j0 >= d || !live) continue;
-      float g[N], n[N];
-      unpack_chunk<T>(*slot(stage, 0, c), g);
-      unpack_chunk<T>(*slot(stage, 1, c), n);
+      for (int c = 0; c < kChunks; ++c) {
+        if (!at.any(c)) continue;
+        float2 g[P], n[P];
+        unpack_pairs<T>(load_slot(stage + c * kPitch), g);
+        unpack_pairs<T>(load_slot(stage + (kChunks + c) * kPitch), n);
 #pragma unroll
-      for (int i = 0; i < N; ++i) g[i] = (g[i] * w[c * N + i] - s.x - (n[i] - mu) * r * s.y) * r;
-      if (add) {
-        unpack_chunk<T>(*slot(stage, 2, c), n);
+        for (int i = 0; i < P; ++i)
+          g[i] = fma2(mul2(add2(n[i], m2), r2), c2, fma2(g[i], w[c * P + i], m1));
+        if (add) {
+          unpack_pairs<T>(load_slot(stage + (2 * kChunks + c) * kPitch), n);
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] += n[i];
+          for (int i = 0; i < P; ++i) g[i] = fma2(g[i], r2, n[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) g[i] = mul2(g[i], r2);
+        }
+        at.store(dx, c, pack_pairs<T>(g));
       }
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + t * d + j0) = pack_chunk<T>(g);
     }
+    t += step;
+    dx += step * a.d;
     mu = next_mu;
     r = next_r;
-    stage = stage == S - 1 ? 0 : stage + 1;
+    next = stage;
+    stage = stage + stage_bytes == own + S * stage_bytes ? own : stage + stage_bytes;
   }
-  if (a.want_w || a.want_b)
-    write_partial<kChunks * N>(a, sw, sb, reinterpret_cast<float*>(ring),
-                               [&](int i) { return (lane + i / N * a.tpr) * N + i % N; });
+  auto column = [&](int i) { return at.j0[i / (2 * P)] + i % (2 * P); };
+  auto part = [](const float2* v, int i) { return i & 1 ? v[i >> 1].y : v[i >> 1].x; };
+  float* shared = reinterpret_cast<float*>(ring);
+  if (a.want_w)
+    write_partial<kChunks * 2 * P>(a, 0, kAligned, shared, [&](int i) { return part(sw, i); }, column);
+  if (a.want_b)
+    write_partial<kChunks * 2 * P>(a, 1, kAligned, shared, [&](int i) { return part(sb, i); }, column);
 }
 
 template <typename T, int kValues>
@@ -501,8 +602,10 @@ __global__ void __launch_bounds__(512) backward_values_kernel(const BackwardArgs
       static_cast<T*>(a.dx)[row * a.d + j] = from_f32<T>(v);
     }
   }
-  if (a.want_w || a.want_b)
-    write_partial<kValues>(a, sw, sb, reinterpret_cast<float*>(ring), [&](int i) { return lane + i * a.tpr; });
+  auto column = [&](int i) { return lane + i * a.tpr; };
+  float* shared = reinterpret_cast<float*>(ring);
+  if (a.want_w) write_partial<kValues>(a, 0, true, shared, [&](int i) { return sw[i]; }, column);
+  if (a.want_b) write_partial<kValues>(a, 1, true, shared, [&](int i) { return sb[i]; }, column);
 }
 
 // Rows too long for the registers: dx by a block a row in two sweeps, and
@@ -570,10 +673,6 @@ __global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ 
 }
 
 // ---- host
-bool rows_on_chunks(const void* p, int64_t stride, int64_t T, int esize) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (T <= 1 || (stride * esize) % 16 == 0);
-}
-
 // Threads (a power of two) for a row of `units` chunks or values: up to a
 // warp, one each; then as few as hold the row with `most` each.
 int threads_per_row(int units, int most) {
@@ -595,25 +694,61 @@ cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t b
   return err;
 }
 
-template <int kChunks>
-constexpr size_t ring_bytes(int operands, int block) {
-  return static_cast<size_t>(kStages<kChunks>) * operands * kChunks * 16 * block;
-}
-
 int grid_of(int64_t T, int groups, int most) {
   const int64_t want = (T + groups - 1) / groups;
   return static_cast<int>(want < most ? want : most);
 }
 
-template <typename T, int kChunks>
-cudaError_t forward_ring(const ForwardArgs& a, int block, int num_sms, cudaStream_t stream) {
+// Blocks of a ring kernel: one an SM.  With rows that do not start on a
+// chunk, all blocks together take a multiple of `values` rows a round
+// (`values` is a power of two, and so is the number of groups).
+int ring_grid(int64_t T, int tpr, int values, bool aligned, int num_sms) {
+  const int groups = kRingThreads / tpr;
+  const int multiple = aligned || groups >= values ? 1 : values / groups;
+  const int grid = grid_of(T, groups, num_sms);
+  const int up = (grid + multiple - 1) / multiple * multiple;
+  return up <= num_sms ? up : num_sms / multiple * multiple;
+}
+
+template <typename T, int kChunks, bool kAligned>
+cudaError_t forward_ring(const ForwardArgs& a, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(forward_ring_kernel<T, kChunks>), done,
-                                     ring_bytes<kChunks>(2, kRingThreads));
+  constexpr size_t operand = static_cast<size_t>(kForwardStages<kChunks>) * kChunks * kPitch;
+  const cudaError_t err =
+      allow_smem(reinterpret_cast<const void*>(forward_ring_kernel<T, kChunks, kAligned>), done, 2 * operand);
   if (err != cudaSuccess) return err;
-  const int grid = grid_of(a.T, block / a.tpr, num_sms * (kRingThreads / block));
-  forward_ring_kernel<T, kChunks><<<grid, block, ring_bytes<kChunks>(a.res.ptr ? 2 : 1, block), stream>>>(a);
+  forward_ring_kernel<T, kChunks, kAligned>
+      <<<ring_grid(a.T, a.tpr, kChunk<T>, kAligned, num_sms), kRingThreads, (a.res.ptr ? 2 : 1) * operand, stream>>>(a);
   return cudaGetLastError();
+}
+
+// How rows lie: on chunks, or all alike within 16 bytes, or neither.  Each
+// operand's base and row stride in bytes.
+struct Lie {
+  bool on_chunks = true, alike = true;
+  uintptr_t base0;
+  int64_t stride0;
+  Lie(const void* p, int64_t stride_bytes) : base0(reinterpret_cast<uintptr_t>(p)), stride0(stride_bytes) {
+    add(p, stride_bytes);
+  }
+  void add(const void* p, int64_t stride_bytes) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(p);
+    if (base % 16 != 0 || stride_bytes % 16 != 0) on_chunks = false;
+    if ((base - base0) % 16 != 0 || (stride_bytes - stride0) % 16 != 0) alike = false;
+  }
+};
+
+bool param_on_chunks(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Threads for a ring's row, or 0 where 3 chunks a thread do not hold it.  A
+// row that does not start on a chunk may touch one more than it fills, and
+// has at least 8 threads (its groups' column sums are added one by one).
+int ring_threads(int d, int values, bool aligned, int* per_thread) {
+  const int chunks = (d + values - 1) / values + (aligned ? 0 : 1);
+  int tpr = threads_per_row(chunks, 3);
+  if (!aligned && tpr < 8) tpr = 8;
+  *per_thread = (chunks + tpr - 1) / tpr;
+  return tpr <= kRingThreads ? tpr : 0;
 }
 
 template <typename T, int kValues>
@@ -626,20 +761,24 @@ cudaError_t forward_values(const ForwardArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t forward_typed(ForwardArgs& a, int num_sms, cudaStream_t stream) {
   constexpr int N = kChunk<T>, e = sizeof(T);
-  const int wsize = a.w_f32 ? 4 : e;
-  const int chunks = (a.d + N - 1) / N;
-  const bool on_chunks = a.d % N == 0 && rows_on_chunks(a.x.ptr, a.x.stride, a.T, e) &&
-                         (!a.res.ptr || rows_on_chunks(a.res.ptr, a.res.stride, a.T, e)) &&
-                         rows_on_chunks(a.y, a.d, a.T, e) && rows_on_chunks(a.z, a.d, a.T, e) &&
-                         rows_on_chunks(a.w, 0, 1, wsize) && rows_on_chunks(a.b, 0, 1, wsize);
-  if (on_chunks && chunks <= 3 * kRingThreads) {
-    a.tpr = threads_per_row(chunks, 3);
-    const int block = a.tpr < 256 ? 256 : a.tpr;
-    switch ((chunks + a.tpr - 1) / a.tpr) {
-      case 1: return forward_ring<T, 1>(a, block, num_sms, stream);
-      case 2: return forward_ring<T, 2>(a, block, num_sms, stream);
-      default: return forward_ring<T, 3>(a, block, num_sms, stream);
+  Lie lie(a.x.ptr, a.T > 1 ? a.x.stride * e : a.d * e);
+  lie.add(a.y, static_cast<int64_t>(a.d) * e);
+  if (a.res.ptr) {
+    lie.add(a.res.ptr, a.T > 1 ? a.res.stride * e : a.d * e);
+    lie.add(a.z, static_cast<int64_t>(a.d) * e);
+  }
+  const bool aligned = lie.on_chunks && a.d % N == 0 && param_on_chunks(a.w) && param_on_chunks(a.b);
+  int per_thread = 0;
+  if (aligned || lie.alike) a.tpr = ring_threads(a.d, N, aligned, &per_thread);
+  if (a.tpr > 0) {
+    if (aligned) {
+      if (per_thread == 1) return forward_ring<T, 1, true>(a, num_sms, stream);
+      if (per_thread == 2) return forward_ring<T, 2, true>(a, num_sms, stream);
+      return forward_ring<T, 3, true>(a, num_sms, stream);
     }
+    if (per_thread == 1) return forward_ring<T, 1, false>(a, num_sms, stream);
+    if (per_thread == 2) return forward_ring<T, 2, false>(a, num_sms, stream);
+    return forward_ring<T, 3, false>(a, num_sms, stream);
   }
   // at most 8 values a thread: more spill at 1,024 threads
   a.tpr = threads_per_row(a.d, 8);
@@ -649,16 +788,16 @@ cudaError_t forward_typed(ForwardArgs& a, int num_sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, int kChunks>
-cudaError_t backward_ring(const BackwardArgs& a, int block, int num_sms, int* blocks, cudaStream_t stream) {
+template <typename T, int kChunks, bool kAligned>
+cudaError_t backward_ring(const BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(backward_ring_kernel<T, kChunks>), done,
-                                     ring_bytes<kChunks>(3, kRingThreads));
+  constexpr size_t operand = static_cast<size_t>(kBackwardStages<kChunks>) * kChunks * kPitch;
+  const cudaError_t err =
+      allow_smem(reinterpret_cast<const void*>(backward_ring_kernel<T, kChunks, kAligned>), done, 3 * operand);
   if (err != cudaSuccess) return err;
-  const int most = num_sms * (kRingThreads / block);
-  *blocks = grid_of(a.T, block / a.tpr, most < kNormMaxBlocks ? most : kNormMaxBlocks);
-  backward_ring_kernel<T, kChunks>
-      <<<*blocks, block, ring_bytes<kChunks>(a.dz.ptr ? 3 : 2, block), stream>>>(a);
+  *blocks = ring_grid(a.T, a.tpr, kChunk<T>, kAligned, num_sms);
+  backward_ring_kernel<T, kChunks, kAligned>
+      <<<*blocks, kRingThreads, (a.dz.ptr ? 3 : 2) * operand, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -676,19 +815,22 @@ cudaError_t backward_values(const BackwardArgs& a, int num_sms, int* blocks, cud
 template <typename T>
 cudaError_t backward_typed(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
   constexpr int N = kChunk<T>, e = sizeof(T);
-  const int chunks = (a.d + N - 1) / N;
-  const bool on_chunks = a.d % N == 0 && rows_on_chunks(a.dy.ptr, a.dy.stride, a.T, e) &&
-                         rows_on_chunks(a.z.ptr, a.z.stride, a.T, e) &&
-                         (!a.dz.ptr || rows_on_chunks(a.dz.ptr, a.dz.stride, a.T, e)) &&
-                         rows_on_chunks(a.dx, a.d, a.T, e) && rows_on_chunks(a.w, 0, 1, a.w_f32 ? 4 : e);
-  if (on_chunks && chunks <= 3 * kRingThreads) {
-    a.tpr = threads_per_row(chunks, 3);
-    const int block = a.tpr < 256 ? 256 : a.tpr;
-    switch ((chunks + a.tpr - 1) / a.tpr) {
-      case 1: return backward_ring<T, 1>(a, block, num_sms, blocks, stream);
-      case 2: return backward_ring<T, 2>(a, block, num_sms, blocks, stream);
-      default: return backward_ring<T, 3>(a, block, num_sms, blocks, stream);
+  Lie lie(a.dy.ptr, a.T > 1 ? a.dy.stride * e : a.d * e);
+  lie.add(a.z.ptr, a.T > 1 ? a.z.stride * e : a.d * e);
+  if (a.dz.ptr) lie.add(a.dz.ptr, a.T > 1 ? a.dz.stride * e : a.d * e);
+  lie.add(a.dx, static_cast<int64_t>(a.d) * e);
+  const bool aligned = lie.on_chunks && a.d % N == 0 && param_on_chunks(a.w);
+  int per_thread = 0;
+  if (aligned || lie.alike) a.tpr = ring_threads(a.d, N, aligned, &per_thread);
+  if (a.tpr > 0) {
+    if (aligned) {
+      if (per_thread == 1) return backward_ring<T, 1, true>(a, num_sms, blocks, stream);
+      if (per_thread == 2) return backward_ring<T, 2, true>(a, num_sms, blocks, stream);
+      return backward_ring<T, 3, true>(a, num_sms, blocks, stream);
     }
+    if (per_thread == 1) return backward_ring<T, 1, false>(a, num_sms, blocks, stream);
+    if (per_thread == 2) return backward_ring<T, 2, false>(a, num_sms, blocks, stream);
+    return backward_ring<T, 3, false>(a, num_sms, blocks, stream);
   }
   a.tpr = threads_per_row(a.d, a.d <= 2048 ? 8 : 16);
   if (a.tpr <= kRingThreads) {

@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
+#include "launch.cuh"
 
 namespace moe {
 namespace {
@@ -26,7 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kScaleBlock = 128;
 constexpr int kChunkValues = kThreads * 8;       // one vector a thread
-constexpr int kNormChunkValues = kThreads * 32;  // four
+constexpr int kNormVectors = 4;                  // 32-byte vectors a thread of the gradient norm's chunk
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTinyBlock = 7.888609052210118e-31f;  // 2^-100
 
@@ -91,12 +92,6 @@ __device__ __forceinline__ void load8_f32(const float* p, uint32_t (&w)[8]) {
                : "l"(p));
 }
 
-__device__ __forceinline__ void store8_f32(float* p, const float (&v)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
 __device__ __forceinline__ void load8(const void* p, int type, int64_t i, Raw8& r) {
   if (type == MOE_F32) {
     load8_f32(static_cast<const float*>(p) + i, r.w);
@@ -107,23 +102,25 @@ __device__ __forceinline__ void load8(const void* p, int type, int64_t i, Raw8& 
   }
 }
 
-__device__ __forceinline__ void values8(const Raw8& r, int type, float (&v)[8]) {
+__device__ __forceinline__ void values8(const Raw8& r, int type, float2 (&v)[4]) {
   if (type == MOE_F32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
   } else {
     const uint4 u = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-    if (type == MOE_BF16) unpack_chunk<__nv_bfloat16>(u, v);
-    else unpack_chunk<__half>(u, v);
+    if (type == MOE_BF16) unpack_pairs<__nv_bfloat16>(u, v);
+    else unpack_pairs<__half>(u, v);
   }
 }
 
-__device__ __forceinline__ void store8(void* p, int type, int64_t i, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* p, int type, int64_t i, const float2 (&v)[4]) {
   if (type == MOE_F32) {
-    store8_f32(static_cast<float*>(p) + i, v);
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(p) + i),
+                 "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+                 : "memory");
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-        type == MOE_BF16 ? pack_chunk<__nv_bfloat16>(v) : pack_chunk<__half>(v);
+        type == MOE_BF16 ? pack_pairs<__nv_bfloat16>(v) : pack_pairs<__half>(v);
   }
 }
 
@@ -145,38 +142,49 @@ __device__ __forceinline__ void block_scale(float amax, float* scale, float* inv
   *inv = tiny ? 1.0f : __fdiv_rn(kE4M3Max, amax);
 }
 
-// Products and sums rounded singly; the new moments and the new parameter.
-__device__ __forceinline__ void adamw_value(const moe_adamw_hyper_t& h, float decay, float g, float& p, float& m,
-                                            float& v, float& root) {
-  m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.one_minus_beta1));
-  v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.one_minus_beta2));
-  root = __fsqrt_rn(v);
-  // the quotient goes into a sum that rounds away far more than its two ulps
-  const float update = __fdividef(m * h.step_size, root * h.inv_sqrt_bias + h.eps);
-  p = p - (p * decay + update);
+// A quotient for the update, which goes into a sum that rounds away far more
+// than its two ulps.  Denormal arguments count as zero: a root of a positive
+// second moment is above 1e-23.
+__device__ __forceinline__ float divide_approx(float a, float b) {
+  float r;
+  asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The sum of two products rounded on their own: as single additions, because
+// the assembler merges a packed addition with the packed product before it.
+__device__ __forceinline__ float2 add_single(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// The new moments (products and sums rounded singly), the root of the second
+// and the new parameter of two values.
+__device__ __forceinline__ void adamw_pair(const moe_adamw_hyper_t& h, float decay, float2 g, float2& p, float2& m,
+                                           float2& v, float2& root) {
+  m = add_single(mul2(m, both(h.beta1)), mul2(g, both(h.one_minus_beta1)));
+  v = add_single(mul2(v, both(h.beta2)), mul2(mul2(g, g), both(h.one_minus_beta2)));
+  root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 denom = fma2(root, both(h.inv_sqrt_bias), both(h.eps));
+  const float2 num = mul2(m, both(h.step_size));
+  const float2 update = make_float2(divide_approx(num.x, denom.x), divide_approx(num.y, denom.y));
+  const float2 change = fma2(p, both(decay), update);
+  p = fma2(change, both(-1.0f), p);
 }
 
 // E4M3 codes of eight values, four to a word.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-  uint32_t w[2];
+__device__ __forceinline__ uint2 encode8(const float2 (&x)[4], float inv) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 lo = make_float2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv));
-    const float2 hi = make_float2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv));
-    w[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3)) |
-           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3)) << 16;
-  }
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(mul2(x[i], both(inv)), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-__device__ __forceinline__ void decode8(const uint2& codes, float scale, float (&v)[8]) {
+__device__ __forceinline__ void decode8(const uint2& codes, float scale, float2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t word = i < 2 ? codes.x : codes.y;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<uint16_t>(word >> (16 * (i & 1))), __NV_E4M3);
-    const float2 f = __half22float2(__half2(h));
-    v[2 * i] = __fmul_rn(f.x, scale);
-    v[2 * i + 1] = __fmul_rn(f.y, scale);
+    v[i] = mul2(__half22float2(__half2(h)), both(scale));
   }
 }
 
@@ -205,32 +213,32 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   const float factor = factor_p ? *factor_p : 1.0f;
   if (!isfinite(factor)) return;
   const float decay = h.decay * t.decay;
-  float g[8], p[8], m[8], v[8], root[8];
+  float2 g[4], p[4], m[4], v[4], root[4];
   values8(raw_g, t.grad_type, g);
   values8(raw_p, p_type, p);
   if (kBits8) {
     decode8(code_m, ms, m);
     decode8(code_v, vs, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], v[i]);
+  } else {
+    values8(raw_m, MOE_F32, m);
+    values8(raw_v, MOE_F32, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) adamw_pair(h, decay, mul2(g[i], both(factor)), p[i], m[i], v[i], root[i]);
+  if (master) store8(t.master, MOE_F32, j, p);
+  store8(t.param, t.param_type, j, p);
+  if (!kBits8) {
+    store8(t.m, MOE_F32, j, m);
+    store8(t.v, MOE_F32, j, v);
+    return;
   }
   float m_max = 0.0f, v_max = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (kBits8) {
-      v[i] = __fmul_rn(v[i], v[i]);
-    } else {
-      m[i] = __uint_as_float(raw_m.w[i]);
-      v[i] = __uint_as_float(raw_v.w[i]);
-    }
-    adamw_value(h, decay, __fmul_rn(g[i], factor), p[i], m[i], v[i], root[i]);
-    m_max = max_nan(m_max, fabsf(m[i]));
-    v_max = max_nan(v_max, root[i]);
-  }
-  if (master) store8_f32(t.master + j, p);
-  store8(t.param, t.param_type, j, p);
-  if (!kBits8) {
-    store8_f32(static_cast<float*>(t.m) + j, m);
-    store8_f32(static_cast<float*>(t.v) + j, v);
-    return;
+  for (int i = 0; i < 4; ++i) {
+    m_max = max_nan(m_max, max_nan(fabsf(m[i].x), fabsf(m[i].y)));
+    v_max = max_nan(v_max, max_nan(root[i].x, root[i].y));
   }
 #pragma unroll
   for (int s = 8; s > 0; s >>= 1) {
@@ -242,11 +250,13 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   block_scale(v_max, &v_scale, &v_inv);
   *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = encode8(m, m_inv);
   uint2 codes = encode8(root, v_inv);
+  if (__vcmpeq4(codes.x, 0) | __vcmpeq4(codes.y, 0)) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t& w = i < 4 ? codes.x : codes.y;
-    const uint32_t one = 1u << (8 * (i & 3));
-    if ((w & (one * 255u)) == 0 && root[i] > 0.0f) w |= one;
+    for (int i = 0; i < 8; ++i) {
+      uint32_t& w = i < 4 ? codes.x : codes.y;
+      const uint32_t one = 1u << (8 * (i & 3));
+      if ((w & (one * 255u)) == 0 && (i & 1 ? root[i / 2].y : root[i / 2].x) > 0.0f) w |= one;
+    }
   }
   *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
   if ((threadIdx.x & 15) == 0) {
@@ -285,7 +295,9 @@ __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_ad
         m[i] = static_cast<const float*>(t.m)[j];
         v = static_cast<const float*>(t.v)[j];
       }
-      adamw_value(h, decay, g, p, m[i], v, root[i]);
+      float2 p2 = both(p), m2 = both(m[i]), v2 = both(v), root2;
+      adamw_pair(h, decay, both(g), p2, m2, v2, root2);
+      p = p2.x, m[i] = m2.x, v = v2.x, root[i] = root2.x;
       if (t.master) t.master[j] = p;
       store_any(t.param, t.param_type, j, p);
       if (!t.bits8) {
@@ -343,56 +355,71 @@ __device__ double block_sum(double v, double* red) {
   return total;
 }
 
-// A block takes chunks blockIdx.x, + gridDim.x, ...; the vectors of a tensor
-// start at its first 32-byte boundary, and the values before it go with the
-// first chunk.
+// A block takes chunks blockIdx.x, + gridDim.x, ... of kNormVectors 32-byte
+// vectors a thread; the vectors of a tensor start at its first 32-byte
+// boundary, and the values before it go with the first chunk.
 template <int kCapacity>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ List<kCapacity> list,
                                                            double* __restrict__ partial) {
   __shared__ double red[kThreads / 32];
-  constexpr int kPer = kNormChunkValues / (kThreads * 8);
-  float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  let_next_start();
+  float2 s[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+  float odd = 0.0f;
   for (int chunk = blockIdx.x; chunk < list.chunks; chunk += gridDim.x) {
     const int which = tensor_of(list, chunk);
     const Tensor& t = list.t[which];
-    const int esize = t.grad_type == MOE_F32 ? 4 : 2;
+    const int esize = t.grad_type == MOE_F32 ? 4 : 2, per = 32 / esize;
     const int64_t head = static_cast<int64_t>((32 - (reinterpret_cast<uintptr_t>(t.grad) & 31)) & 31) / esize;
-    const int64_t begin = head + static_cast<int64_t>(chunk - list.first[which]) * kNormChunkValues;
-    if (chunk == list.first[which])
-      for (int64_t j = threadIdx.x; j < head && j < t.n; j += kThreads) {
-        const float g = load_any(t.grad, t.grad_type, j);
-        s[0] += g * g;
-      }
-    Raw8 raw[kPer];
+    const int64_t begin = head + static_cast<int64_t>(chunk - list.first[which]) * (kNormVectors * kThreads * per);
+    uint32_t raw[kNormVectors][8];
+    const int64_t left = t.n - begin;  // values from the chunk's begin
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t j = begin + (i * kThreads + threadIdx.x) * 8;
-      if (j + 8 <= t.n) load8(t.grad, t.grad_type, j, raw[i]);
+    for (int i = 0; i < kNormVectors; ++i) {
+      const int at = (i * kThreads + threadIdx.x) * per;
+      if (at + per <= left)
+        load8_f32(reinterpret_cast<const float*>(static_cast<const char*>(t.grad) + (begin + at) * esize), raw[i]);
+      else
+#pragma unroll
+        for (int k = 0; k < 8; ++k) raw[i][k] = 0;
     }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int64_t j = begin + (i * kThreads + threadIdx.x) * 8;
-      if (j + 8 <= t.n) {
-        float g[8];
-        values8(raw[i], t.grad_type, g);
+    for (int i = 0; i < kNormVectors; ++i) {
+      if (t.grad_type == MOE_F32) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[k] += g[k] * g[k];
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = make_float2(__uint_as_float(raw[i][2 * k]), __uint_as_float(raw[i][2 * k + 1]));
+          s[k] = fma2(g, g, s[k]);
+        }
       } else {
-        for (int64_t k = j; k < t.n; ++k) {
-          const float g = load_any(t.grad, t.grad_type, k);
-          s[0] += g * g;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float f[2];
+          if (t.grad_type == MOE_BF16) Word<__nv_bfloat16>::unpack(raw[i][k], f);
+          else Word<__half>::unpack(raw[i][k], f);
+          const float2 g = make_float2(f[0], f[1]);
+          s[k & 3] = fma2(g, g, s[k & 3]);
         }
       }
     }
+    // the values before the first vector, and those after the last whole one
+    if (chunk == list.first[which] && threadIdx.x < head && threadIdx.x < t.n) {
+      const float g = load_any(t.grad, t.grad_type, threadIdx.x);
+      odd += g * g;
+    }
+    if (left > 0 && left < kNormVectors * kThreads * per && threadIdx.x < left % per) {
+      const float g = load_any(t.grad, t.grad_type, t.n - 1 - threadIdx.x);
+      odd += g * g;
+    }
   }
-  const float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-  const double total = block_sum(sum, red);
+  const float2 all = add2(add2(s[0], s[1]), add2(s[2], s[3]));
+  const double total = block_sum(all.x + all.y + odd, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict__ partial, int blocks, float max_norm,
                                                         float* __restrict__ out) {
   __shared__ double red[kThreads / 32];
+  wait_for_previous();
   double s = 0.0;
   for (int b = threadIdx.x; b < blocks; b += kThreads) s += partial[b];
   s = block_sum(s, red);
@@ -412,12 +439,13 @@ bool all_aligned(const moe_adamw_tensor_t& s) {
 }
 
 template <int kCapacity>
-int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, int chunk_values, int* at) {
+int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, bool norm, int* at) {
   list.count = 0;
   int64_t chunks = 0;
   while (*at < n_tensors && list.count < kCapacity) {
     const moe_adamw_tensor_t& s = tensors[*at];
-    const int64_t more = (s.n + chunk_values - 1) / chunk_values;
+    const int chunk = !norm ? kChunkValues : kNormVectors * kThreads * 32 / (s.grad_type == MOE_F32 ? 4 : 2);
+    const int64_t more = (s.n + chunk - 1) / chunk;
     if (chunks + more > INT32_MAX) break;
     ++*at;
     if (s.n == 0) continue;
@@ -439,7 +467,7 @@ cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const mo
   list.hyper_dev = hyper_dev;
   list.grad_scale = grad_scale;
   for (int at = 0; at < n_tensors;) {
-    if (fill(list, tensors, n_tensors, kChunkValues, &at) == 0) continue;
+    if (fill(list, tensors, n_tensors, false, &at) == 0) continue;
     adamw_kernel<kCapacity><<<list.chunks, kThreads, 0, stream>>>(list);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
@@ -457,7 +485,7 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
   if (most < 1) return cudaErrorInvalidValue;
   int blocks = 0;
   for (int at = 0; at < n_tensors;) {
-    const int chunks = fill(list, tensors, n_tensors, kNormChunkValues, &at);
+    const int chunks = fill(list, tensors, n_tensors, true, &at);
     if (chunks == 0) continue;
     const int grid = chunks < most ? chunks : most;
     if (blocks + grid > kGradNormMaxBlocks) return cudaErrorInvalidValue;
@@ -466,8 +494,11 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
     if (err != cudaSuccess) return err;
     blocks += grid;
   }
-  norm_kernel<<<1, kThreads, 0, stream>>>(partial, blocks, max_norm, out);
-  return cudaGetLastError();
+  if (blocks == 0) {  // nothing to add up: the kernel has no other to wait for
+    norm_kernel<<<1, kThreads, 0, stream>>>(partial, blocks, max_norm, out);
+    return cudaGetLastError();
+  }
+  return launch_dependent(norm_kernel, 1, kThreads, 0, stream, partial, blocks, max_norm, out);
 }
 
 // Capacities of the kernels' lists: a call takes the smallest that holds its

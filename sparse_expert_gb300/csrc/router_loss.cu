@@ -13,8 +13,8 @@
 //
 // A group of `tpr` lanes (a power of two, up to a warp) holds a row: vectors
 // of four values lane, lane + tpr, ... where rows and E allow 16-byte
-// accesses, else single values.  Warps walk over the rows with the next
-// row's loads in flight.
+// accesses, else single values.  Enough warps are resident to cover a row's
+// loads by the others' arithmetic, which runs on pairs of values.
 //
 // The mask is counted by a kernel of its own first: every block needs N, and
 // each counting for itself (in the first version) cost more than the losses
@@ -87,23 +87,32 @@ __device__ __forceinline__ int column(int i, int lane, int tpr) {
 
 template <int kValues, bool kVec>
 __device__ __forceinline__ void load_row(const float* row, bool live, float fill, int E, int lane, int tpr,
-                                         float (&v)[kValues]) {
+                                         float2 (&v)[kValues / 2]) {
 #pragma unroll
-  for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
+  for (int i = 0; i < kValues; i += kVec ? 4 : 2) {
     const int e = column<kVec>(i, lane, tpr);
     if (kVec) {
       float4 q = make_float4(fill, fill, fill, fill);
       if (live && e < E) q = *reinterpret_cast<const float4*>(row + e);
-      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+      v[i / 2] = make_float2(q.x, q.y);
+      v[i / 2 + 1] = make_float2(q.z, q.w);
     } else {
-      v[i] = live && e < E ? row[e] : fill;
+      v[i / 2].x = live && e < E ? row[e] : fill;
+      v[i / 2].y = live && e + tpr < E ? row[e + tpr] : fill;
     }
   }
 }
 
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int kValues, bool kVec>
-__global__ void __launch_bounds__(kThreads) loss_kernel(const Args args) {
+__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 4 : 2) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
+  constexpr int kPairsRow = kValues / 2;
   const int tpr = args.tpr, E = a.E;
   __shared__ int64_t red_i[kThreads / 32];
   __shared__ double red[kThreads / 32];
@@ -112,82 +121,80 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const Args args) {
   int64_t counted = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) counted += a.counts[e];
   counted = block_sum(counted, red_i);
-  float share[kValues];
+  // fp32 quotients: counts and their total are exact to 24 bits
+  const float total = static_cast<float>(counted);
+  float2 share[kPairsRow];
 #pragma unroll
   for (int i = 0; i < kValues; ++i) {
     const int e = column<kVec>(i, lane, tpr);
-    share[i] = e < E && counted > 0 ? static_cast<float>(a.counts[e] / static_cast<double>(counted)) : 0.0f;
+    const float q = e < E && counted > 0 ? static_cast<float>(a.counts[e]) / total : 0.0f;
+    if (i & 1) share[i / 2].y = q;
+    else share[i / 2].x = q;
   }
-  const float cb = a.balance_coef * static_cast<float>(E), cz = 2.0f * a.z_coef;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
-  int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr;
-  const int64_t rounds = (a.T - static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + step - 1) / step;
-  bool live = t < a.T && (!a.mask || a.mask[t] != 0);
-  float l[kValues], before[kValues];
-  load_row<kValues, kVec>(a.logits + t * E, live, -INFINITY, E, lane, tpr, l);
-  if (a.d_in) load_row<kValues, kVec>(a.d_in + t * E, live, 0.0f, E, lane, tpr, before);
   int64_t n = a.T;
   if (args.kept) {
     wait_for_previous();
-    n = 0;
-    for (int i = 0; i < kCountBlocks; ++i) n += args.kept[i];
+    int64_t part = threadIdx.x < kCountBlocks ? args.kept[threadIdx.x] : 0;
+    n = block_sum(part, red_i);
   }
-  const float inv_n = n > 0 ? static_cast<float>(1.0 / static_cast<double>(n)) : 0.0f;
+  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+  const float cb = a.balance_coef * static_cast<float>(E), cz = 2.0f * a.z_coef;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
   float sum_s = 0.0f, sum_z = 0.0f;
-  for (int64_t round = 0; round < rounds; ++round, t += step) {
-    // the next row, before this one is used
-    const int64_t next = t + step;
-    const bool next_live = next < a.T && (!a.mask || a.mask[next] != 0);
-    float next_l[kValues], next_before[kValues];
-    load_row<kValues, kVec>(a.logits + next * E, next_live, -INFINITY, E, lane, tpr, next_l);
-    if (a.d_in) load_row<kValues, kVec>(a.d_in + next * E, next_live, 0.0f, E, lane, tpr, next_before);
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr); first < a.T; first += step) {
+    const int64_t t = first + threadIdx.x / tpr;
+    const bool row = t < a.T;
+    const bool live = row && (!a.mask || a.mask[t] != 0);
+    // a masked row of a gradient accumulated in place is left as it is
+    const bool write = row && (live || !a.d_in || a.d_in != a.d_logits);
+    float2 l[kPairsRow], before[kPairsRow];
+    load_row<kValues, kVec>(a.logits + t * E, live, -INFINITY, E, lane, tpr, l);
+    if (a.d_in) load_row<kValues, kVec>(a.d_in + t * E, write, 0.0f, E, lane, tpr, before);
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) top = fmaxf(top, l[i]);
+    for (int i = 0; i < kPairsRow; ++i) top = fmaxf(top, fmaxf(l[i].x, l[i].y));
     top = group_max(top, tpr);
-    const bool empty = top == -INFINITY;  // masked, or every logit is -infinity
-    float z = 0.0f, dot = 0.0f;
+    // a row without a finite or infinite logit above -infinity (masked, or
+    // every expert taken out) is shifted by 0: its exponentials are zero.  A
+    // NaN makes z, and so the row's gradient and both losses, NaN
+    const float2 shift = both(top == -INFINITY ? 0.0f : -top);
+    float2 z2 = both(0.0f), dot2 = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      // a NaN logit makes z, and so the row's gradient and both losses, NaN
-      const float e = empty && l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
-      l[i] = e;
-      z += e;
-      dot += e * share[i];
+    for (int i = 0; i < kPairsRow; ++i) {
+      const float2 e = mul2(add2(l[i], shift), both(kLog2e));
+      l[i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+      z2 = add2(z2, l[i]);
+      dot2 = fma2(l[i], share[i], dot2);
     }
-    z = group_sum(z, tpr);
-    dot = group_sum(dot, tpr);
-    const float inv_z = empty && z == 0.0f ? 0.0f : 1.0f / z;
+    const float z = group_sum(z2.x + z2.y, tpr), dot = group_sum(dot2.x + dot2.y, tpr);
+    const bool empty = z == 0.0f;
+    const float inv_z = empty ? 0.0f : 1.0f / z;
     const float s = dot * inv_z;
-    const float lse = empty && z == 0.0f ? 0.0f : top + logf(z);
+    const float lse = empty ? 0.0f : top + logf(z);
     sum_s += s;
     sum_z += lse * lse;
-    // a masked row of an accumulated gradient is left as it is
-    if (t < a.T && (live || !a.d_in || a.d_in != a.d_logits)) {
-      const float zl = cz * lse, scale = inv_z * inv_n;
-      float* row = a.d_logits + t * E;
+    if (!write) continue;
+    // p / N (cb (share - s) + cz lse) = e (scale_b share + scale_0)
+    const float scale = inv_z * inv_n;
+    const float2 scale_b = both(scale * cb), scale_0 = both(scale * (cz * lse - cb * s));
+    float* out = a.d_logits + t * E;
 #pragma unroll
-      for (int i = 0; i < kValues; ++i) {
-        l[i] = live ? l[i] * scale * (cb * (share[i] - s) + zl) : 0.0f;
-        if (a.d_in) {
-          const int e = column<kVec>(i, lane, tpr);
-          if (!live && e < E) before[i] = a.d_in[t * E + e];
-          l[i] += before[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
-        const int e = column<kVec>(i, lane, tpr);
-        if (e >= E) continue;
-        if (kVec) *reinterpret_cast<float4*>(row + e) = make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
-        else row[e] = l[i];
-      }
+    for (int i = 0; i < kPairsRow; ++i) {
+      l[i] = mul2(l[i], fma2(scale_b, share[i], scale_0));
+      if (a.d_in) l[i] = add2(l[i], before[i]);
     }
-    live = next_live;
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) {
-      l[i] = next_l[i];
-      before[i] = next_before[i];
+    for (int i = 0; i < kValues; i += kVec ? 4 : 2) {
+      const int e = column<kVec>(i, lane, tpr);
+      const float2 lo = l[i / 2];
+      if (kVec) {
+        const float2 hi = l[i / 2 + (kVec ? 1 : 0)];
+        if (e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        if (e < E) out[e] = lo.x;
+        if (e + tpr < E) out[e + tpr] = lo.y;
+      }
     }
   }
   // every lane of a group carries the row's sums: one of them counts
