@@ -147,7 +147,12 @@ __device__ __forceinline__ uint4 add_chunks(const uint4& a, const uint4& b) {
 // Sum over the aligned group of `width` (a power of two up to 32) lanes that
 // the calling lane belongs to, the same value on each.
 __device__ __forceinline__ float group_sum(float v, int width) {
-  for (int s = width >> 1; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  if (width == 32) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  } else {
+    for (int s = width >> 1; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  }
   return v;
 }
 

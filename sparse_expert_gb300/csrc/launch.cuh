@@ -1,16 +1,88 @@
+// Launch forms of the training-step kernels.
+//
 // Programmatic dependent launch: a kernel that follows another on the same
 // stream may be brought onto the SMs before the first one has ended.  The
 // second kernel calls wait_for_previous() before it reads anything that the
 // first one writes (the wait covers the whole first grid and its writes);
 // the first one calls let_next_start() as early as it likes.
+//
+// One cluster: a small problem runs as a single cluster of up to kClusterMost
+// blocks that add their sums through each other's shared memory, which saves
+// the second launch and its scratch (the time of a small call is the host's).
 #pragma once
 
+#include <atomic>
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace moe {
 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+constexpr int kClusterMost = 16;  // above 8 needs the kernel's leave (allow_cluster)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all blocks of the cluster; writes to shared memory before it
+// are visible after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Reads of another block's shared memory, at the caller's own address of it.
+__device__ __forceinline__ uint32_t remote_addr(const void* own, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(own))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float remote_f32(const float* own, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr(own, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ double remote_f64(const double* own, uint32_t rank) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote_addr(own, rank)) : "memory");
+  return v;
+}
+
+// Lets the kernel have `smem` bytes of dynamic shared memory and clusters of
+// kClusterMost blocks, once for each device.
+inline cudaError_t allow(const void* kernel, std::atomic<uint64_t>& done, size_t smem, bool cluster) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (smem > 0)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (err == cudaSuccess && cluster)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), int blocks, int threads, size_t smem, cudaStream_t stream,
+                           Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

@@ -28,8 +28,6 @@
 // difference of two sums, so a large common offset costs no digits.  Sums
 // are fp32 per thread and then trees over lanes and warps, always in the same
 // order.
-#include <atomic>
-
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -66,34 +64,62 @@ struct BackwardArgs {
   int d;
   void* dx;
   float* partial;  // [blocks][2][d]: the block's sums of dy n, and of dy
+  float* dw;  // the sums over all blocks, where one cluster holds them
+  float* db;
   bool want_w, want_b;
   int tpr;
+  int cluster;  // blocks of that cluster, or 0: the sums go to `partial`
 };
 
 constexpr int kMaxWarps = 32;
 
-// Sums over the row's group, in every thread of it.  `red` is one of two
-// buffers used in turn: a thread reaches the next sum's barrier only after
-// it has read this one's buffer, so one barrier a sum is enough.
-__device__ __forceinline__ float2 group_reduce(float2 v, int tpr, float2* red) {
-  for (int s = (tpr < 32 ? tpr : 32) >> 1; s > 0; s >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
-  }
-  if (tpr <= 32) return v;
-  const int lane = threadIdx.x & 31, warps = tpr >> 5, first = threadIdx.x / tpr * warps;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / tpr), "r"(tpr) : "memory");
-  v = red[first + (lane & (warps - 1))];
-  for (int s = warps >> 1; s > 0; s >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
+__device__ __forceinline__ float shuffle_add(float v, int s) { return v + __shfl_xor_sync(0xffffffffu, v, s); }
+__device__ __forceinline__ float2 shuffle_add(float2 v, int s) {
+  return make_float2(shuffle_add(v.x, s), shuffle_add(v.y, s));
+}
+
+// Sum over the lanes of a warp that belong to the row: all of them, or the
+// aligned group of tpr.
+template <typename V>
+__device__ __forceinline__ V warp_reduce(V v, int tpr) {
+  if (tpr >= 32) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) v = shuffle_add(v, s);
+  } else {
+    for (int s = tpr >> 1; s > 0; s >>= 1) v = shuffle_add(v, s);
   }
   return v;
 }
 
+// Tree over the group's warps, whose values lie in lanes modulo `warps`.
+template <typename V>
+__device__ __forceinline__ V over_warps(V v, int warps) {
+#pragma unroll
+  for (int s = kMaxWarps / 2; s > 0; s >>= 1)
+    if (s < warps) v = shuffle_add(v, s);
+  return v;
+}
+
+// Hands each warp's value to the whole group: the calling lane gets that of
+// warp lane mod warps.  `red` is one of two buffers used in turn: a thread
+// reaches the next exchange's barrier only after it has read this one's
+// buffer, so one barrier each is enough.
+__device__ __forceinline__ float2 exchange(float2 v, int tpr, float2* red) {
+  const int lane = threadIdx.x & 31, warps = tpr >> 5, group = threadIdx.x / tpr;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  return red[group * warps + (lane & (warps - 1))];
+}
+
+// Sums over the row's group, in every thread of it.
+__device__ __forceinline__ float2 group_reduce(float2 v, int tpr, float2* red) {
+  v = warp_reduce(v, tpr);
+  return tpr <= 32 ? v : over_warps(exchange(v, tpr, red), tpr >> 5);
+}
+
 __device__ __forceinline__ float group_reduce(float v, int tpr, float2* red) {
-  return group_reduce(make_float2(v, 0.0f), tpr, red).x;
+  v = warp_reduce(v, tpr);
+  return tpr <= 32 ? v : over_warps(exchange(make_float2(v, 0.0f), tpr, red).x, tpr >> 5);
 }
 
 template <typename T>
@@ -119,11 +145,6 @@ __device__ __forceinline__ uint4 load_slot(uint32_t slot) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot));
   return u;
 }
-__device__ __forceinline__ void store_slot(uint32_t slot, const uint4& u) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
-               : "memory");
-}
-
 // One block of 512 threads an SM.  Rows in flight, by a thread's chunks a
 // row: what the SM's shared memory holds with two operands (forward) or
 // three (backward): at most 432 bytes a thread.
@@ -245,6 +266,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
     at.params(c, a.b, a.w_f32, 0.0f, b + c * P);
   }
   const float inv_d = 1.0f / static_cast<float>(a.d);
+  // Mean and variance take one exchange: a warp (or a group inside one) takes
+  // the deviations from its own mean, and the warps' sums q_i of their n_i
+  // values about their means m_i join as q = sum q_i + n_i (m_i - mu)^2.
+  int count = 0;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    if (at.any(c)) count += min(at.j0[c] + 2 * P, a.d) - max(at.j0[c], 0);
+  const float n_warp = warp_reduce(static_cast<float>(count), a.tpr);
+  const float inv_n = n_warp > 0.0f ? 1.0f / n_warp : 0.0f;
+  float n_other = 0.0f, inv_other = 0.0f;  // of the warp that exchange() hands over
+  if (a.tpr > 32) {
+    const float2 other = exchange(make_float2(n_warp, inv_n), a.tpr, red[1]);
+    n_other = other.x, inv_other = other.y;
+  }
   uint32_t stage = own, next = own + (S - 1) * stage_bytes;
   T* y = static_cast<T*>(a.y) + t * a.d;
   T* z_row = static_cast<T*>(a.z) + t * a.d;
@@ -252,7 +287,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
     fetch(next);
     copy_wait<S - 1>();
     const bool live = t < a.T;
-    float2 s = both(0.0f);
+    float2 v[kChunks * P], s = both(0.0f);
     if (live) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
@@ -262,47 +297,52 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
           // the sum is rounded to the rows' type here: it is what the caller
           // keeps and what the backward normalises again
           u = add_chunks<T>(u, load_slot(stage + (kChunks + c) * kPitch));
-          store_slot(stage + c * kPitch, u);
           at.store(z_row, c, u);
         }
-        float2 v[P];
-        unpack_pairs<T>(u, v);
-        at.mask(c, v, 0.0f);
+        unpack_pairs<T>(u, v + c * P);
+        at.mask(c, v + c * P, 0.0f);
 #pragma unroll
-        for (int i = 0; i < P; ++i) s = add2(s, v[i]);
+        for (int i = 0; i < P; ++i) s = add2(s, v[c * P + i]);
       }
     }
-    const float mu = group_reduce(s.x + s.y, a.tpr, red[0]) * inv_d;
+    const float sum = warp_reduce(s.x + s.y, a.tpr);
+    const float mid = sum * inv_n;  // the warp's mean
     s = both(0.0f);
     if (live) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!at.any(c)) continue;
-        float2 v[P];
-        unpack_pairs<T>(load_slot(stage + c * kPitch), v);
-        at.mask(c, v, mu);
+        at.mask(c, v + c * P, mid);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          const float2 e = add2(v[i], both(-mu));
+          float2& e = v[c * P + i];
+          e = add2(e, both(-mid));
           s = fma2(e, e, s);
         }
       }
     }
-    const float r = 1.0f / sqrtf(group_reduce(s.x + s.y, a.tpr, red[1]) * inv_d + a.eps);
+    float q = warp_reduce(s.x + s.y, a.tpr), mu = mid;
+    if (a.tpr > 32) {
+      const float2 other = exchange(make_float2(sum, q), a.tpr, red[round & 1]);
+      mu = over_warps(other.x, a.tpr >> 5) * inv_d;
+      const float e = other.x * inv_other - mu;
+      q = over_warps(fmaf(n_other * e, e, other.y), a.tpr >> 5);
+    }
+    const float r = rsqrtf(fmaf(q, inv_d, a.eps));
     if (live) {
       if (lane == 0) {
         a.stats[t] = mu;
         a.stats[a.T + t] = r;
       }
+      const float2 r2 = both(r), shift = both((mid - mu) * r);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         if (!at.any(c)) continue;
-        float2 v[P];
-        unpack_pairs<T>(load_slot(stage + c * kPitch), v);
+        // (z - mu) r = (z - mid) r + (mid - mu) r
 #pragma unroll
         for (int i = 0; i < P; ++i)
-          v[i] = fma2(mul2(add2(v[i], both(-mu)), both(r)), w[c * P + i], b[c * P + i]);
-        at.store(y, c, pack_pairs<T>(v));
+          v[c * P + i] = fma2(fma2(v[c * P + i], r2, shift), w[c * P + i], b[c * P + i]);
+        at.store(y, c, pack_pairs<T>(v + c * P));
       }
     }
     t += step;
@@ -353,7 +393,7 @@ __global__ void __launch_bounds__(1024) forward_values_kernel(const ForwardArgs 
 #pragma unroll
   for (int i = 0; i < kValues; ++i)
     if (lane + i * a.tpr < d) s += (v[i] - mu) * (v[i] - mu);
-  const float r = 1.0f / sqrtf(group_reduce(s, a.tpr, red[1]) * inv_d + a.eps);
+  const float r = rsqrtf(group_reduce(s, a.tpr, red[1]) * inv_d + a.eps);
   if (live && lane == 0) {
     a.stats[t] = mu;
     a.stats[a.T + t] = r;
@@ -395,7 +435,7 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const ForwardArgs a)
     const float e = to_f32(in[j]) - mu;
     s += e * e;
   }
-  const float r = 1.0f / sqrtf(group_reduce(s, blockDim.x, red[1]) / static_cast<float>(a.d) + a.eps);
+  const float r = rsqrtf(group_reduce(s, blockDim.x, red[1]) / static_cast<float>(a.d) + a.eps);
   if (threadIdx.x == 0) {
     a.stats[t] = mu;
     a.stats[a.T + t] = r;
@@ -411,7 +451,30 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const ForwardArgs a)
 // The block's column sums from its threads': where the lanes of a warp own
 // the same columns (`same`: tpr below 32, rows that start alike) they add by
 // a tree, then the warps or groups in order through `shared` (slots x d
-// floats).  column(i): value i's column.
+// floats).  column(i): value i's column.  In a cluster the block's sums stay
+// in shared memory behind the slots, 2 x d floats.
+__device__ __forceinline__ float* cluster_sums(const BackwardArgs& a, bool same, float* shared) {
+  const int slots = blockDim.x / (same && a.tpr < 32 ? 32 : a.tpr);
+  return shared + (slots > 1 ? slots * a.d : 0);
+}
+
+// dw and db from the sums of a cluster's blocks: each block takes every
+// cluster-th run of threads' columns and adds the blocks' sums in order.
+__device__ __forceinline__ void finish_cluster(const BackwardArgs& a, bool same, float* shared) {
+  const float* sums = cluster_sums(a, same, shared);
+  cluster_sync();
+  for (int which = 0; which < 2; ++which) {
+    float* out = which ? a.db : a.dw;
+    if (!out) continue;
+    for (int j = cluster_rank() * blockDim.x + threadIdx.x; j < a.d; j += a.cluster * blockDim.x) {
+      float s = 0.0f;
+      for (int k = 0; k < a.cluster; ++k) s += remote_f32(sums + which * a.d + j, k);
+      out[j] = s;
+    }
+  }
+  cluster_sync();  // no block leaves while another reads its sums
+}
+
 template <int kValues, typename Value, typename Column>
 __device__ __forceinline__ void write_partial(const BackwardArgs& a, int which, bool same, float* shared, Value value,
                                               Column column) {
@@ -419,7 +482,8 @@ __device__ __forceinline__ void write_partial(const BackwardArgs& a, int which, 
   const int width = same && tpr < 32 ? 32 : tpr;  // threads whose sums share a slot
   const int slots = blockDim.x / width, slot = threadIdx.x / width;
   const bool owner = threadIdx.x % width < tpr;
-  float* out = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * d;
+  float* out = a.cluster ? cluster_sums(a, same, shared) + which * d
+                         : a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + which) * d;
   __syncthreads();  // the ring, or the other sum, is done with `shared`
 #pragma unroll
   for (int i = 0; i < kValues; ++i) {
@@ -440,6 +504,7 @@ __device__ __forceinline__ void write_partial(const BackwardArgs& a, int which, 
 template <typename T, int kChunks, bool kAligned>
 __global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const BackwardArgs a) {
   constexpr int P = kPairs<T>, S = kBackwardStages<kChunks>;
+  constexpr bool kKeep = kChunks * P <= 8;  // at most 16 values a thread
   extern __shared__ uint4 ring[];  // [stage][operand][chunk][thread]
   __shared__ float2 red[2][kMaxWarps];
   let_next_start();
@@ -490,6 +555,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const Ba
     const bool live = t < a.T;
     const float2 m2 = both(-mu), r2 = both(r);
     float2 s1 = both(0.0f), s2 = both(0.0f);
+    // the row's n and g w, kept over the exchange where the registers hold
+    // them beside the column sums, else made again from the slots
+    float2 n_row[kKeep ? kChunks * P : 1], gw_row[kKeep ? kChunks * P : 1];
     if (live) {
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
@@ -507,6 +575,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const Ba
           g[i] = mul2(g[i], w[c * P + i]);
           s1 = add2(s1, g[i]);
           s2 = fma2(g[i], n[i], s2);
+          if (kKeep) {
+            n_row[kKeep ? c * P + i : 0] = n[i];
+            gw_row[kKeep ? c * P + i : 0] = g[i];
+          }
         }
       }
     }
@@ -517,11 +589,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const Ba
       for (int c = 0; c < kChunks; ++c) {
         if (!at.any(c)) continue;
         float2 g[P], n[P];
-        unpack_pairs<T>(load_slot(stage + c * kPitch), g);
-        unpack_pairs<T>(load_slot(stage + (kChunks + c) * kPitch), n);
+        if (kKeep) {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          g[i] = fma2(mul2(add2(n[i], m2), r2), c2, fma2(g[i], w[c * P + i], m1));
+          for (int i = 0; i < P; ++i)
+            g[i] = fma2(n_row[kKeep ? c * P + i : 0], c2, add2(gw_row[kKeep ? c * P + i : 0], m1));
+        } else {
+          unpack_pairs<T>(load_slot(stage + c * kPitch), g);
+          unpack_pairs<T>(load_slot(stage + (kChunks + c) * kPitch), n);
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            g[i] = fma2(mul2(add2(n[i], m2), r2), c2, fma2(g[i], w[c * P + i], m1));
+        }
         if (add) {
           unpack_pairs<T>(load_slot(stage + (2 * kChunks + c) * kPitch), n);
 #pragma unroll
@@ -547,6 +625,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) backward_ring_kernel(const Ba
     write_partial<kChunks * 2 * P>(a, 0, kAligned, shared, [&](int i) { return part(sw, i); }, column);
   if (a.want_b)
     write_partial<kChunks * 2 * P>(a, 1, kAligned, shared, [&](int i) { return part(sb, i); }, column);
+  if (a.cluster) finish_cluster(a, kAligned, shared);
 }
 
 template <typename T, int kValues>
@@ -606,6 +685,7 @@ __global__ void __launch_bounds__(512) backward_values_kernel(const BackwardArgs
   float* shared = reinterpret_cast<float*>(ring);
   if (a.want_w) write_partial<kValues>(a, 0, true, shared, [&](int i) { return sw[i]; }, column);
   if (a.want_b) write_partial<kValues>(a, 1, true, shared, [&](int i) { return sb[i]; }, column);
+  if (a.cluster) finish_cluster(a, true, shared);
 }
 
 // Rows too long for the registers: dx by a block a row in two sweeps, and
@@ -682,18 +762,6 @@ int threads_per_row(int units, int most) {
   return tpr;
 }
 
-// Lifts the kernel's shared-memory limit, once for each device.
-cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done, size_t bytes) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return err;
-}
-
 int grid_of(int64_t T, int groups, int most) {
   const int64_t want = (T + groups - 1) / groups;
   return static_cast<int>(want < most ? want : most);
@@ -715,7 +783,7 @@ cudaError_t forward_ring(const ForwardArgs& a, int num_sms, cudaStream_t stream)
   static std::atomic<uint64_t> done{0};
   constexpr size_t operand = static_cast<size_t>(kForwardStages<kChunks>) * kChunks * kPitch;
   const cudaError_t err =
-      allow_smem(reinterpret_cast<const void*>(forward_ring_kernel<T, kChunks, kAligned>), done, 2 * operand);
+      allow(reinterpret_cast<const void*>(forward_ring_kernel<T, kChunks, kAligned>), done, 2 * operand, false);
   if (err != cudaSuccess) return err;
   forward_ring_kernel<T, kChunks, kAligned>
       <<<ring_grid(a.T, a.tpr, kChunk<T>, kAligned, num_sms), kRingThreads, (a.res.ptr ? 2 : 1) * operand, stream>>>(a);
@@ -788,26 +856,52 @@ cudaError_t forward_typed(ForwardArgs& a, int num_sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Blocks of the one cluster that takes T rows, or 0 where they are more than
+// 2 rounds of the largest (further rounds cost more than the second launch
+// that the cluster saves: 160 x 2816 in 3 rounds 11.3 us on the GPU, as two
+// launches 7.9 us).
+int cluster_blocks(int64_t T, int groups, int multiple) {
+  if (T > static_cast<int64_t>(groups) * kClusterMost * 2) return 0;
+  const int want = grid_of(T, groups, kClusterMost);
+  int blocks = 1;
+  while (blocks < want || blocks % multiple != 0) blocks *= 2;
+  return blocks;
+}
+
 template <typename T, int kChunks, bool kAligned>
-cudaError_t backward_ring(const BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
+cudaError_t backward_ring(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t operand = static_cast<size_t>(kBackwardStages<kChunks>) * kChunks * kPitch;
   const cudaError_t err =
-      allow_smem(reinterpret_cast<const void*>(backward_ring_kernel<T, kChunks, kAligned>), done, 3 * operand);
+      allow(reinterpret_cast<const void*>(backward_ring_kernel<T, kChunks, kAligned>), done, 3 * operand, true);
   if (err != cudaSuccess) return err;
+  const size_t smem = (a.dz.ptr ? 3 : 2) * operand;
+  const int groups = kRingThreads / a.tpr;
+  const int multiple = kAligned || groups >= kChunk<T> ? 1 : kChunk<T> / groups;
+  a.cluster = cluster_blocks(a.T, groups, multiple);
+  if (a.cluster)
+    return launch_cluster(backward_ring_kernel<T, kChunks, kAligned>, a.cluster, kRingThreads, smem, stream, a);
   *blocks = ring_grid(a.T, a.tpr, kChunk<T>, kAligned, num_sms);
-  backward_ring_kernel<T, kChunks, kAligned>
-      <<<*blocks, kRingThreads, (a.dz.ptr ? 3 : 2) * operand, stream>>>(a);
+  backward_ring_kernel<T, kChunks, kAligned><<<*blocks, kRingThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int kValues>
-cudaError_t backward_values(const BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
+cudaError_t backward_values(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
   const int block = a.tpr < 256 ? 256 : a.tpr, groups = block / a.tpr;
+  const int slots = a.tpr < 32 ? block / 32 : groups;
+  size_t smem = slots > 1 ? static_cast<size_t>(slots) * a.d * 4 : 0;  // at most 8 x 256 floats
+  a.cluster = cluster_blocks(a.T, groups, 1);
+  if (a.cluster) {
+    smem += static_cast<size_t>(2) * a.d * 4;
+    const cudaError_t err = allow(reinterpret_cast<const void*>(backward_values_kernel<T, kValues>), done,
+                                  static_cast<size_t>(8 * 256 + 2 * kRingThreads * kValues) * 4, true);
+    if (err != cudaSuccess) return err;
+    return launch_cluster(backward_values_kernel<T, kValues>, a.cluster, block, smem, stream, a);
+  }
   const int most = num_sms * (kRingThreads / block);
   *blocks = grid_of(a.T, groups, most < kNormMaxBlocks ? most : kNormMaxBlocks);
-  const int slots = a.tpr < 32 ? block / 32 : groups;
-  const size_t smem = slots > 1 ? static_cast<size_t>(slots) * a.d * 4 : 0;  // at most 8 x 256 floats
   backward_values_kernel<T, kValues><<<*blocks, block, smem, stream>>>(a);
   return cudaGetLastError();
 }
@@ -866,7 +960,8 @@ cudaError_t launch_layer_norm(const NormForward& f, int num_sms, cudaStream_t st
 
 cudaError_t launch_layer_norm_backward(const NormBackward& f, int num_sms, cudaStream_t stream) {
   BackwardArgs a{{f.dy, f.dy_stride}, {f.z, f.z_stride}, {f.dz, f.dz_stride}, f.stats, f.weight,
-                 f.weight_dtype == MOE_F32, f.T, f.d, f.dx, f.partial, f.dweight != nullptr, f.dbias != nullptr, 0};
+                 f.weight_dtype == MOE_F32, f.T, f.d, f.dx, f.partial, f.dweight, f.dbias, f.dweight != nullptr,
+                 f.dbias != nullptr, 0, 0};
   int blocks = 0;
   cudaError_t err;
   switch (f.dtype) {
@@ -874,7 +969,7 @@ cudaError_t launch_layer_norm_backward(const NormBackward& f, int num_sms, cudaS
     case MOE_BF16: err = backward_typed<__nv_bfloat16>(a, num_sms, &blocks, stream); break;
     default: err = backward_typed<__half>(a, num_sms, &blocks, stream); break;
   }
-  if (err != cudaSuccess || !(a.want_w || a.want_b)) return err;
+  if (err != cudaSuccess || a.cluster || !(a.want_w || a.want_b)) return err;
   return launch_dependent(finish_kernel, dim3((f.d + 31) / 32, 2), 1024, 0, stream, f.partial, blocks, f.d, f.dweight,
                           f.dbias);
 }

@@ -24,9 +24,11 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kBlockThreads = 256;
+constexpr int kClusterThreads = 1024;  // of a block of the gradient norm's one cluster
 constexpr int kScaleBlock = 128;
-constexpr int kChunkValues = kThreads * 8;       // one vector a thread
+constexpr int kChunkValues = kBlockThreads * 8;       // one vector a thread
+constexpr int kClusterRounds = 2;                     // chunks of a block of the gradient norm's one cluster
 constexpr int kNormVectors = 4;                  // 32-byte vectors a thread of the gradient norm's chunk
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTinyBlock = 7.888609052210118e-31f;  // 2^-100
@@ -274,7 +276,7 @@ __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_ad
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float decay = h.decay * t.decay;
   for (int64_t b0 = begin + warp * kScaleBlock; b0 < t.n && b0 < begin + kChunkValues;
-       b0 += kScaleBlock * (kThreads / 32)) {
+       b0 += kScaleBlock * (kBlockThreads / 32)) {
     const int64_t block = b0 / kScaleBlock;
     const float ms = t.bits8 ? t.m_scale[block] : 1.0f, vs = t.bits8 ? t.v_scale[block] : 1.0f;
     float m[4], root[4];
@@ -333,7 +335,7 @@ __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_ad
 }
 
 template <int kCapacity>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
+__global__ void __launch_bounds__(kBlockThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
   const moe_adamw_hyper_t h = list.hyper_dev ? *list.hyper_dev : list.hyper;
   const int which = tensor_of(list, blockIdx.x);
   const Tensor& t = list.t[which];
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 }
 
 // ---- gradient norm
+// Sum over the block in a fixed order, in thread 0.
 __device__ double block_sum(double v, double* red) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
@@ -351,17 +354,24 @@ __device__ double block_sum(double v, double* red) {
   __syncthreads();
   double total = 0.0;
   if (threadIdx.x == 0)
-    for (int i = 0; i < kThreads / 32; ++i) total += red[i];
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) total += red[i];
   return total;
+}
+
+__device__ __forceinline__ void write_norm(double squares, float max_norm, float* out) {
+  const double norm = sqrt(squares);
+  out[0] = static_cast<float>(norm);
+  out[1] = !isfinite(out[0]) ? nanf("") : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.0f;
 }
 
 // A block takes chunks blockIdx.x, + gridDim.x, ... of kNormVectors 32-byte
 // vectors a thread; the vectors of a tensor start at its first 32-byte
 // boundary, and the values before it go with the first chunk.
-template <int kCapacity>
+// As one cluster (`out` given), its first block writes the result.
+template <int kCapacity, int kThreads>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ List<kCapacity> list,
-                                                           double* __restrict__ partial) {
-  __shared__ double red[kThreads / 32];
+                                                           double* __restrict__ partial, float max_norm, float* out) {
+  __shared__ double red[kThreads / 32], block_squares;
   let_next_start();
   float2 s[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
   float odd = 0.0f;
@@ -413,21 +423,28 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
   }
   const float2 all = add2(add2(s[0], s[1]), add2(s[2], s[3]));
   const double total = block_sum(all.x + all.y + odd, red);
-  if (threadIdx.x == 0) partial[blockIdx.x] = total;
+  if (!out) {
+    if (threadIdx.x == 0) partial[blockIdx.x] = total;
+    return;
+  }
+  if (threadIdx.x == 0) block_squares = total;
+  cluster_sync();
+  if (cluster_rank() == 0 && threadIdx.x == 0) {
+    double squares = 0.0;
+    for (uint32_t k = 0; k < gridDim.x; ++k) squares += remote_f64(&block_squares, k);
+    write_norm(squares, max_norm, out);
+  }
+  cluster_sync();  // no block leaves while another reads its sum
 }
 
-__global__ void __launch_bounds__(kThreads) norm_kernel(const double* __restrict__ partial, int blocks, float max_norm,
+__global__ void __launch_bounds__(kBlockThreads) norm_kernel(const double* __restrict__ partial, int blocks, float max_norm,
                                                         float* __restrict__ out) {
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kBlockThreads / 32];
   wait_for_previous();
   double s = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += kThreads) s += partial[b];
+  for (int b = threadIdx.x; b < blocks; b += kBlockThreads) s += partial[b];
   s = block_sum(s, red);
-  if (threadIdx.x == 0) {
-    const double norm = sqrt(s);
-    out[0] = static_cast<float>(norm);
-    out[1] = !isfinite(out[0]) ? nanf("") : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.0f;
-  }
+  if (threadIdx.x == 0) write_norm(s, max_norm, out);
 }
 
 // ---- lists
@@ -439,12 +456,13 @@ bool all_aligned(const moe_adamw_tensor_t& s) {
 }
 
 template <int kCapacity>
-int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, bool norm, int* at) {
+int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors, int norm_threads, int* at) {
   list.count = 0;
   int64_t chunks = 0;
   while (*at < n_tensors && list.count < kCapacity) {
     const moe_adamw_tensor_t& s = tensors[*at];
-    const int chunk = !norm ? kChunkValues : kNormVectors * kThreads * 32 / (s.grad_type == MOE_F32 ? 4 : 2);
+    const int chunk =
+        norm_threads == 0 ? kChunkValues : kNormVectors * norm_threads * 32 / (s.grad_type == MOE_F32 ? 4 : 2);
     const int64_t more = (s.n + chunk - 1) / chunk;
     if (chunks + more > INT32_MAX) break;
     ++*at;
@@ -467,8 +485,8 @@ cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const mo
   list.hyper_dev = hyper_dev;
   list.grad_scale = grad_scale;
   for (int at = 0; at < n_tensors;) {
-    if (fill(list, tensors, n_tensors, false, &at) == 0) continue;
-    adamw_kernel<kCapacity><<<list.chunks, kThreads, 0, stream>>>(list);
+    if (fill(list, tensors, n_tensors, 0, &at) == 0) continue;
+    adamw_kernel<kCapacity><<<list.chunks, kBlockThreads, 0, stream>>>(list);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
@@ -478,27 +496,40 @@ cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const mo
 template <int kCapacity>
 cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out, double* partial,
                      int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
   List<kCapacity> list{};
   const int launches = (n_tensors + kCapacity - 1) / kCapacity;
-  int most = num_sms * 8;
+  int most = num_sms * 5;
   if (launches > 0 && most > kGradNormMaxBlocks / launches) most = kGradNormMaxBlocks / launches;
   if (most < 1) return cudaErrorInvalidValue;
   int blocks = 0;
+  if (launches == 1) {
+    int at = 0;
+    const int chunks = fill(list, tensors, n_tensors, kClusterThreads, &at);
+    if (at == n_tensors && chunks <= kClusterMost * kClusterRounds) {
+      auto kernel = squares_kernel<kCapacity, kClusterThreads>;
+      const cudaError_t err = allow(reinterpret_cast<const void*>(kernel), done, 0, true);
+      if (err != cudaSuccess) return err;
+      int cluster = 1;
+      while (cluster < chunks && cluster < kClusterMost) cluster *= 2;
+      return launch_cluster(kernel, cluster, kClusterThreads, 0, stream, list, partial, max_norm, out);
+    }
+  }
   for (int at = 0; at < n_tensors;) {
-    const int chunks = fill(list, tensors, n_tensors, true, &at);
+    const int chunks = fill(list, tensors, n_tensors, kBlockThreads, &at);
     if (chunks == 0) continue;
     const int grid = chunks < most ? chunks : most;
     if (blocks + grid > kGradNormMaxBlocks) return cudaErrorInvalidValue;
-    squares_kernel<kCapacity><<<grid, kThreads, 0, stream>>>(list, partial + blocks);
+    squares_kernel<kCapacity, kBlockThreads><<<grid, kBlockThreads, 0, stream>>>(list, partial + blocks, max_norm, nullptr);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     blocks += grid;
   }
   if (blocks == 0) {  // nothing to add up: the kernel has no other to wait for
-    norm_kernel<<<1, kThreads, 0, stream>>>(partial, blocks, max_norm, out);
+    norm_kernel<<<1, kBlockThreads, 0, stream>>>(partial, blocks, max_norm, out);
     return cudaGetLastError();
   }
-  return launch_dependent(norm_kernel, 1, kThreads, 0, stream, partial, blocks, max_norm, out);
+  return launch_dependent(norm_kernel, 1, kBlockThreads, 0, stream, partial, blocks, max_norm, out);
 }
 
 // Capacities of the kernels' lists: a call takes the smallest that holds its

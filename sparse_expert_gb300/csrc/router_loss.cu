@@ -13,12 +13,14 @@
 //
 // A group of `tpr` lanes (a power of two, up to a warp) holds a row: vectors
 // of four values lane, lane + tpr, ... where rows and E allow 16-byte
-// accesses, else single values.  Enough warps are resident to cover a row's
-// loads by the others' arithmetic, which runs on pairs of values.
+// accesses, else single values.  Groups walk over the rows; a lane copies its
+// own values of the next row into its own slots of shared memory while it
+// works on this one, so no barrier is needed and the loads never pause.
 //
 // The mask is counted by a kernel of its own first: every block needs N, and
 // each counting for itself (in the first version) cost more than the losses
-// (65,536 tokens: 349 us in all).
+// (65,536 tokens: 349 us in all).  A small problem is one cluster of blocks
+// that count, and add up the losses, among themselves: one launch.
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -33,12 +35,18 @@ constexpr int kCountBlocks = 64;
 struct Args {
   RouterLoss a;
   const int32_t* kept;  // [kCountBlocks] tokens kept, by the counting kernel; null without a mask
-  double* partial;      // [blocks][2]
+  double* partial;      // [blocks][2], unless one cluster adds up the losses
   int tpr;
+  int cluster;          // its blocks, or 0
 };
 
 __device__ __forceinline__ float group_max(float v, int width) {
-  for (int s = width >> 1; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+  if (width == 32) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+  } else {
+    for (int s = width >> 1; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+  }
   return v;
 }
 
@@ -85,20 +93,43 @@ __device__ __forceinline__ int column(int i, int lane, int tpr) {
   return kVec ? ((i >> 2) * tpr + lane) * 4 + (i & 3) : i * tpr + lane;
 }
 
+// A lane's slots: 16 bytes a vector, or 4 a value, kThreads lanes apart.
+template <bool kVec>
+constexpr uint32_t kPitch = kThreads * (kVec ? 16 : 4);
+
 template <int kValues, bool kVec>
-__device__ __forceinline__ void load_row(const float* row, bool live, float fill, int E, int lane, int tpr,
+__device__ __forceinline__ void fetch_row(uint32_t slot, const float* row, int E, int lane, int tpr) {
+#pragma unroll
+  for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
+    const int e = column<kVec>(i, lane, tpr);
+    if (e >= E) continue;
+    if (kVec)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i / 4 * kPitch<kVec>), "l"(row + e)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + i * kPitch<kVec>), "l"(row + e) : "memory");
+  }
+}
+
+template <int kValues, bool kVec>
+__device__ __forceinline__ void take_row(uint32_t slot, bool live, float fill, int E, int lane, int tpr,
                                          float2 (&v)[kValues / 2]) {
 #pragma unroll
   for (int i = 0; i < kValues; i += kVec ? 4 : 2) {
     const int e = column<kVec>(i, lane, tpr);
     if (kVec) {
       float4 q = make_float4(fill, fill, fill, fill);
-      if (live && e < E) q = *reinterpret_cast<const float4*>(row + e);
+      if (live && e < E)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                     : "r"(slot + i / 4 * kPitch<kVec>));
       v[i / 2] = make_float2(q.x, q.y);
-      v[i / 2 + 1] = make_float2(q.z, q.w);
+      v[i / 2 + (kVec ? 1 : 0)] = kVec ? make_float2(q.z, q.w) : v[i / 2];
     } else {
-      v[i / 2].x = live && e < E ? row[e] : fill;
-      v[i / 2].y = live && e + tpr < E ? row[e + tpr] : fill;
+      v[i / 2] = both(fill);
+      if (live && e < E) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i / 2].x) : "r"(slot + i * kPitch<kVec>));
+      if (live && e + tpr < E)
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i / 2].y) : "r"(slot + (i + 1) * kPitch<kVec>));
     }
   }
 }
@@ -109,15 +140,44 @@ __device__ __forceinline__ float exp2_approx(float v) {
   return r;
 }
 
+// Rows in flight: this one and the next two where a lane has up to 12 values
+// (3 resident blocks of 74 KB), else the next one.
+template <int kValues>
+constexpr int kStages = kValues <= 12 ? 3 : 2;
+
 template <int kValues, bool kVec>
-__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 4 : 2) loss_kernel(const Args args) {
+__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
-  constexpr int kPairsRow = kValues / 2;
+  constexpr int kPairsRow = kValues / 2, S = kStages<kValues>;
+  constexpr uint32_t kOperand = kValues / (kVec ? 4 : 1) * kPitch<kVec>;
   const int tpr = args.tpr, E = a.E;
+  extern __shared__ uint4 ring[];  // [stage][operand][vector or value][thread]
   __shared__ int64_t red_i[kThreads / 32];
-  __shared__ double red[kThreads / 32];
+  __shared__ double red[kThreads / 32], block_losses[2];
   let_next_start();
   const int lane = threadIdx.x % tpr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr);
+  const int64_t rounds = (a.T - first + step - 1) / step;
+  int64_t t = first + threadIdx.x / tpr;
+  auto kept_row = [&](int64_t row) { return row < a.T && (!a.mask || __ldg(a.mask + row) != 0); };
+  // a masked row of a gradient accumulated in place is left as it is
+  const bool in_place = a.d_in && a.d_in == a.d_logits;
+  const uint32_t own = smem_addr(ring) + threadIdx.x * (kVec ? 16 : 4), stage_bytes = (a.d_in ? 2 : 1) * kOperand;
+  int64_t ahead = t;
+  bool ahead_live = kept_row(ahead);
+  uint32_t live_bits = 0;  // bit k: the row k rounds after this one is kept
+  auto fetch = [&](uint32_t stage, int round) {
+    if (ahead_live) fetch_row<kValues, kVec>(stage, a.logits + ahead * E, E, lane, tpr);
+    if (a.d_in && ahead < a.T && (ahead_live || !in_place))
+      fetch_row<kValues, kVec>(stage + kOperand, a.d_in + ahead * E, E, lane, tpr);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    live_bits |= static_cast<uint32_t>(ahead_live) << round;
+    ahead += step;
+    ahead_live = kept_row(ahead);
+  };
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fetch(own + s * stage_bytes, s);
   int64_t counted = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) counted += a.counts[e];
   counted = block_sum(counted, red_i);
@@ -136,21 +196,25 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 4 : 2) loss_kernel(c
     wait_for_previous();
     int64_t part = threadIdx.x < kCountBlocks ? args.kept[threadIdx.x] : 0;
     n = block_sum(part, red_i);
+  } else if (a.mask) {
+    int64_t part = 0;
+    for (int64_t i = threadIdx.x; i < a.T; i += kThreads) part += a.mask[i] != 0;
+    n = block_sum(part, red_i);
   }
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
   const float cb = a.balance_coef * static_cast<float>(E), cz = 2.0f * a.z_coef;
   constexpr float kLog2e = 1.4426950408889634f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
   float sum_s = 0.0f, sum_z = 0.0f;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr); first < a.T; first += step) {
-    const int64_t t = first + threadIdx.x / tpr;
-    const bool row = t < a.T;
-    const bool live = row && (!a.mask || a.mask[t] != 0);
-    // a masked row of a gradient accumulated in place is left as it is
-    const bool write = row && (live || !a.d_in || a.d_in != a.d_logits);
+  uint32_t stage = own, next = own + (S - 1) * stage_bytes;
+  for (int64_t round = 0; round < rounds; ++round, t += step, live_bits >>= 1) {
+    fetch(next, S - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    const bool row = t < a.T, live = live_bits & 1u, write = row && (live || !in_place);
     float2 l[kPairsRow], before[kPairsRow];
-    load_row<kValues, kVec>(a.logits + t * E, live, -INFINITY, E, lane, tpr, l);
-    if (a.d_in) load_row<kValues, kVec>(a.d_in + t * E, write, 0.0f, E, lane, tpr, before);
+    take_row<kValues, kVec>(stage, live, -INFINITY, E, lane, tpr, l);
+    if (a.d_in) take_row<kValues, kVec>(stage + kOperand, write, 0.0f, E, lane, tpr, before);
+    next = stage;
+    stage = stage + stage_bytes == own + S * stage_bytes ? own : stage + stage_bytes;
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kPairsRow; ++i) top = fmaxf(top, fmaxf(l[i].x, l[i].y));
@@ -169,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 4 : 2) loss_kernel(c
     }
     const float z = group_sum(z2.x + z2.y, tpr), dot = group_sum(dot2.x + dot2.y, tpr);
     const bool empty = z == 0.0f;
-    const float inv_z = empty ? 0.0f : 1.0f / z;
+    const float inv_z = empty ? 0.0f : __fdividef(1.0f, z);  // z in [1, E]
     const float s = dot * inv_z;
-    const float lse = empty ? 0.0f : top + logf(z);
+    const float lse = empty ? 0.0f : top + __logf(z);
     sum_s += s;
     sum_z += lse * lse;
     if (!write) continue;
@@ -200,11 +264,25 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 4 : 2) loss_kernel(c
   // every lane of a group carries the row's sums: one of them counts
   const double s = block_sum(lane == 0 ? static_cast<double>(sum_s) : 0.0, red);
   const double z = block_sum(lane == 0 ? static_cast<double>(sum_z) : 0.0, red);
-  if (threadIdx.x == 0) {
-    const double inv = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
-    args.partial[2 * blockIdx.x] = s * E * inv;
-    args.partial[2 * blockIdx.x + 1] = z * inv;
+  const double inv = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+  if (!args.cluster) {
+    if (threadIdx.x == 0) {
+      args.partial[2 * blockIdx.x] = s * E * inv;
+      args.partial[2 * blockIdx.x + 1] = z * inv;
+    }
+    return;
   }
+  if (threadIdx.x == 0) {
+    block_losses[0] = s * E * inv;
+    block_losses[1] = z * inv;
+  }
+  cluster_sync();
+  if (cluster_rank() == 0 && threadIdx.x < 2) {
+    double sum = 0.0;
+    for (int k = 0; k < args.cluster; ++k) sum += remote_f64(block_losses + threadIdx.x, k);
+    a.losses[threadIdx.x] = static_cast<float>(sum);
+  }
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restrict__ partial, int blocks,
@@ -228,8 +306,14 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
 // result); without it they follow the caller's work as any launch does.
 template <int kValues, bool kVec>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
-  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec>, grid, kThreads, 0, stream, args);
-  loss_kernel<kValues, kVec><<<grid, kThreads, 0, stream>>>(args);
+  static std::atomic<uint64_t> done{0};
+  constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
+  const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec>), done, 2 * operand, true);
+  if (err != cudaSuccess) return err;
+  const size_t smem = (args.a.d_in ? 2 : 1) * operand;
+  if (args.cluster) return launch_cluster(loss_kernel<kValues, kVec>, args.cluster, kThreads, smem, stream, args);
+  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec>, grid, kThreads, smem, stream, args);
+  loss_kernel<kValues, kVec><<<grid, kThreads, smem, stream>>>(args);
   return cudaGetLastError();
 }
 
@@ -250,7 +334,7 @@ size_t router_loss_workspace_bytes() { return align_up(kPartialBytes + kCountBlo
 
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream) {
   auto* kept = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + kPartialBytes);
-  Args args{a, a.mask ? kept : nullptr, static_cast<double*>(a.workspace), 1};
+  Args args{a, nullptr, static_cast<double*>(a.workspace), 1, 0};
   const uintptr_t low = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_in) |
                         reinterpret_cast<uintptr_t>(a.d_logits);
   const bool vec = a.E % 4 == 0 && low % 16 == 0;
@@ -259,10 +343,18 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   const int values = (units + args.tpr - 1) / args.tpr * (vec ? 4 : 1);
   const int groups = kThreads / args.tpr;
   const int64_t want = (a.T + groups - 1) / groups;
-  const int64_t most = num_sms * 4 < kRouterLossMaxBlocks ? num_sms * 4 : kRouterLossMaxBlocks;
-  const int grid = static_cast<int>(want < most ? want : most);
   cudaError_t err;
+  // one cluster up to 2 rounds of the largest: further rounds cost more than
+  // the other launches
+  if (want <= kClusterMost * 2) {
+    args.cluster = 1;
+    while (args.cluster < want && args.cluster < kClusterMost) args.cluster *= 2;
+    return vec ? launch_losses<true>(args, values, 0, stream) : launch_losses<false>(args, values, 0, stream);
+  }
+  const int64_t most = num_sms * (values <= 12 ? 3 : 2);
+  const int grid = static_cast<int>(want < most ? want : most);
   if (a.mask) {
+    args.kept = kept;
     count_kernel<<<kCountBlocks, kThreads, 0, stream>>>(a.mask, a.T, kept);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
