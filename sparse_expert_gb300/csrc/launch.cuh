@@ -6,6 +6,11 @@
 // first one writes (the wait covers the whole first grid and its writes);
 // the first one calls let_next_start() as early as it likes.
 //
+// Stealing blocks: a kernel launched with one block for each piece of work
+// keeps running by cancelling launches that are still waiting and doing their
+// pieces itself (cluster launch control), so pieces go to the SMs as these
+// get free, without a counter in memory and without a new block's start-up.
+//
 // One cluster: a small problem runs as a single cluster of up to kClusterMost
 // blocks that add their sums through each other's shared memory, which saves
 // the second launch and its scratch (the time of a small call is the host's).
@@ -15,10 +20,37 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
+
 namespace moe {
 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Asks for a launch to cancel; the answer (16 bytes, in `answer`) completes the
+// barrier's phase.  One thread; not again after a refusal.
+__device__ __forceinline__ void steal_request(uint4* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_addr(answer)),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+// The x index of the block whose launch was cancelled, or -1.
+__device__ __forceinline__ int steal_answer(const uint4* answer) {
+  uint32_t x = 0, ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, a;\n\t}"
+      : "=r"(x), "=r"(ok)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
+}
 
 constexpr int kClusterMost = 16;  // above 8 needs the kernel's leave (allow_cluster)
 

@@ -43,7 +43,7 @@ struct Tensor {
   float* v_scale;
   int64_t n;
   float decay;
-  uint8_t param_type, grad_type, bits8, vec;  // vec: whole vectors at aligned addresses
+  uint8_t param_type, grad_type, bits8, vec;  // vec: vectors lie at their alignment
 };
 
 template <int kCapacity>
@@ -101,6 +101,18 @@ __device__ __forceinline__ void load8(const void* p, int type, int64_t i, Raw8& 
     asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
                  : "l"(static_cast<const uint16_t*>(p) + i));
+  }
+}
+
+// The first `count` values (of `size` bytes) of the eight, one by one; the
+// rest of the words stays as it is.
+__device__ __forceinline__ void load_some(const void* p, int size, int64_t j, int count, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= count) continue;
+    if (size == 4) w[i] = static_cast<const uint32_t*>(p)[j + i];
+    else if (size == 2) w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[j + i]) << (16 * (i & 1));
+    else w[i / 4] |= static_cast<uint32_t>(static_cast<const uint8_t*>(p)[j + i]) << (8 * (i & 3));
   }
 }
 
@@ -190,27 +202,42 @@ __device__ __forceinline__ void decode8(const uint2& codes, float scale, float2 
   }
 }
 
-// A whole chunk of a tensor with aligned pointers: eight consecutive values
-// a thread, so sixteen lanes hold the 128 values of a scale.
+// A chunk of a tensor with aligned pointers: eight consecutive values a
+// thread, so sixteen lanes hold the 128 values of a scale.  The thread at the
+// tensor's end reads and writes its values one by one, those behind it none
+// (their values are zero and raise no maximum).
 template <bool kBits8>
 __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
                                             int64_t begin) {
   const int64_t j = begin + threadIdx.x * 8;
-  Raw8 raw_g, raw_p, raw_m, raw_v;
-  uint2 code_m, code_v;
-  float ms, vs;
-  load8(t.grad, t.grad_type, j, raw_g);
+  const int count = t.n - j >= 8 ? 8 : t.n > j ? static_cast<int>(t.n - j) : 0;
+  Raw8 raw_g{}, raw_p{}, raw_m{}, raw_v{};
+  uint2 code_m = make_uint2(0, 0), code_v = make_uint2(0, 0);
+  float ms = 0.0f, vs = 0.0f;
   const bool master = t.master != nullptr;
   const int p_type = master ? static_cast<int>(MOE_F32) : t.param_type;
-  load8(master ? t.master : t.param, p_type, j, raw_p);
-  if (kBits8) {
-    code_m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
-    code_v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
+  const void* p_in = master ? t.master : t.param;
+  if (count == 8) {
+    load8(t.grad, t.grad_type, j, raw_g);
+    load8(p_in, p_type, j, raw_p);
+    if (kBits8) {
+      code_m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
+      code_v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
+    } else {
+      load8_f32(static_cast<const float*>(t.m) + j, raw_m.w);
+      load8_f32(static_cast<const float*>(t.v) + j, raw_v.w);
+    }
+  } else {
+    load_some(t.grad, t.grad_type == MOE_F32 ? 4 : 2, j, count, raw_g.w);
+    load_some(p_in, p_type == MOE_F32 ? 4 : 2, j, count, raw_p.w);
+    load_some(t.m, kBits8 ? 1 : 4, j, count, raw_m.w);
+    load_some(t.v, kBits8 ? 1 : 4, j, count, raw_v.w);
+    code_m = make_uint2(raw_m.w[0], raw_m.w[1]);
+    code_v = make_uint2(raw_v.w[0], raw_v.w[1]);
+  }
+  if (kBits8 && count > 0) {
     ms = t.m_scale[j / kScaleBlock];
     vs = t.v_scale[j / kScaleBlock];
-  } else {
-    load8_f32(static_cast<const float*>(t.m) + j, raw_m.w);
-    load8_f32(static_cast<const float*>(t.v) + j, raw_v.w);
   }
   const float factor = factor_p ? *factor_p : 1.0f;
   if (!isfinite(factor)) return;
@@ -229,13 +256,27 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) adamw_pair(h, decay, mul2(g[i], both(factor)), p[i], m[i], v[i], root[i]);
-  if (master) store8(t.master, MOE_F32, j, p);
-  store8(t.param, t.param_type, j, p);
-  if (!kBits8) {
-    store8(t.m, MOE_F32, j, m);
-    store8(t.v, MOE_F32, j, v);
-    return;
+  if (count == 8) {
+    if (master) store8(t.master, MOE_F32, j, p);
+    store8(t.param, t.param_type, j, p);
+    if (!kBits8) {
+      store8(t.m, MOE_F32, j, m);
+      store8(t.v, MOE_F32, j, v);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= count) continue;
+      const float pi = i & 1 ? p[i / 2].y : p[i / 2].x;
+      if (master) t.master[j + i] = pi;
+      store_any(t.param, t.param_type, j + i, pi);
+      if (!kBits8) {
+        static_cast<float*>(t.m)[j + i] = i & 1 ? m[i / 2].y : m[i / 2].x;
+        static_cast<float*>(t.v)[j + i] = i & 1 ? v[i / 2].y : v[i / 2].x;
+      }
+    }
   }
+  if (!kBits8) return;
   float m_max = 0.0f, v_max = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -250,7 +291,7 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   float m_scale, m_inv, v_scale, v_inv;
   block_scale(m_max, &m_scale, &m_inv);
   block_scale(v_max, &v_scale, &v_inv);
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = encode8(m, m_inv);
+  const uint2 m_codes = encode8(m, m_inv);
   uint2 codes = encode8(root, v_inv);
   if (__vcmpeq4(codes.x, 0) | __vcmpeq4(codes.y, 0)) {
 #pragma unroll
@@ -260,15 +301,24 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
       if ((w & (one * 255u)) == 0 && (i & 1 ? root[i / 2].y : root[i / 2].x) > 0.0f) w |= one;
     }
   }
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
-  if ((threadIdx.x & 15) == 0) {
+  if (count == 8) {
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = m_codes;
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= count) continue;
+      static_cast<uint8_t*>(t.m)[j + i] = static_cast<uint8_t>((i < 4 ? m_codes.x : m_codes.y) >> (8 * (i & 3)));
+      static_cast<uint8_t*>(t.v)[j + i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
+    }
+  }
+  if ((threadIdx.x & 15) == 0 && count > 0) {
     t.m_scale[j / kScaleBlock] = m_scale;
     t.v_scale[j / kScaleBlock] = v_scale;
   }
 }
 
-// The last, partial chunk of a tensor, and every chunk of a tensor with
-// other pointers: a warp takes blocks of 128 values, lane + 32 i of each.
+// A chunk of a tensor whose pointers are not all at 32-byte boundaries: a warp takes blocks of 128 values, lane + 32 i of each.
 __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
                                                    int64_t begin) {
   const float factor = factor_p ? *factor_p : 1.0f;
@@ -340,7 +390,7 @@ __global__ void __launch_bounds__(kBlockThreads) adamw_kernel(const __grid_const
   const int which = tensor_of(list, blockIdx.x);
   const Tensor& t = list.t[which];
   const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[which]) * kChunkValues;
-  if (!t.vec || begin + kChunkValues > t.n) adamw_scalar_chunk(t, h, list.grad_scale, begin);
+  if (!t.vec) adamw_scalar_chunk(t, h, list.grad_scale, begin);
   else if (t.bits8) adamw_chunk<true>(t, h, list.grad_scale, begin);
   else adamw_chunk<false>(t, h, list.grad_scale, begin);
 }

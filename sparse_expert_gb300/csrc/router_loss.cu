@@ -97,12 +97,12 @@ __device__ __forceinline__ int column(int i, int lane, int tpr) {
 template <bool kVec>
 constexpr uint32_t kPitch = kThreads * (kVec ? 16 : 4);
 
-template <int kValues, bool kVec>
+template <int kValues, bool kVec, bool kFull>
 __device__ __forceinline__ void fetch_row(uint32_t slot, const float* row, int E, int lane, int tpr) {
 #pragma unroll
   for (int i = 0; i < kValues; i += kVec ? 4 : 1) {
     const int e = column<kVec>(i, lane, tpr);
-    if (e >= E) continue;
+    if (!kFull && e >= E) continue;
     if (kVec)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + i / 4 * kPitch<kVec>), "l"(row + e)
                    : "memory");
@@ -111,7 +111,7 @@ __device__ __forceinline__ void fetch_row(uint32_t slot, const float* row, int E
   }
 }
 
-template <int kValues, bool kVec>
+template <int kValues, bool kVec, bool kFull>
 __device__ __forceinline__ void take_row(uint32_t slot, bool live, float fill, int E, int lane, int tpr,
                                          float2 (&v)[kValues / 2]) {
 #pragma unroll
@@ -119,7 +119,7 @@ __device__ __forceinline__ void take_row(uint32_t slot, bool live, float fill, i
     const int e = column<kVec>(i, lane, tpr);
     if (kVec) {
       float4 q = make_float4(fill, fill, fill, fill);
-      if (live && e < E)
+      if (live && (kFull || e < E))
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
                      : "r"(slot + i / 4 * kPitch<kVec>));
@@ -134,9 +134,10 @@ __device__ __forceinline__ void take_row(uint32_t slot, bool live, float fill, i
   }
 }
 
+// 2^v for -126 <= v (0 below).
 __device__ __forceinline__ float exp2_approx(float v) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -145,7 +146,7 @@ __device__ __forceinline__ float exp2_approx(float v) {
 template <int kValues>
 constexpr int kStages = kValues <= 12 ? 3 : 2;
 
-template <int kValues, bool kVec>
+template <int kValues, bool kVec, bool kFull>
 __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
   constexpr int kPairsRow = kValues / 2, S = kStages<kValues>;
@@ -168,9 +169,9 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
   bool ahead_live = kept_row(ahead);
   uint32_t live_bits = 0;  // bit k: the row k rounds after this one is kept
   auto fetch = [&](uint32_t stage, int round) {
-    if (ahead_live) fetch_row<kValues, kVec>(stage, a.logits + ahead * E, E, lane, tpr);
+    if (ahead_live) fetch_row<kValues, kVec, kFull>(stage, a.logits + ahead * E, E, lane, tpr);
     if (a.d_in && ahead < a.T && (ahead_live || !in_place))
-      fetch_row<kValues, kVec>(stage + kOperand, a.d_in + ahead * E, E, lane, tpr);
+      fetch_row<kValues, kVec, kFull>(stage + kOperand, a.d_in + ahead * E, E, lane, tpr);
     asm volatile("cp.async.commit_group;" ::: "memory");
     live_bits |= static_cast<uint32_t>(ahead_live) << round;
     ahead += step;
@@ -211,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
     const bool row = t < a.T, live = live_bits & 1u, write = row && (live || !in_place);
     float2 l[kPairsRow], before[kPairsRow];
-    take_row<kValues, kVec>(stage, live, -INFINITY, E, lane, tpr, l);
-    if (a.d_in) take_row<kValues, kVec>(stage + kOperand, write, 0.0f, E, lane, tpr, before);
+    take_row<kValues, kVec, kFull>(stage, live, -INFINITY, E, lane, tpr, l);
+    if (a.d_in) take_row<kValues, kVec, kFull>(stage + kOperand, write, 0.0f, E, lane, tpr, before);
     next = stage;
     stage = stage + stage_bytes == own + S * stage_bytes ? own : stage + stage_bytes;
     float top = -INFINITY;
@@ -226,8 +227,11 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
     float2 z2 = both(0.0f), dot2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < kPairsRow; ++i) {
-      const float2 e = mul2(add2(l[i], shift), both(kLog2e));
+      // e^x as the square of 2^(x log2(e) / 2), which stays above the
+      // denormals down to the smallest of them
+      const float2 e = mul2(add2(l[i], shift), both(0.5f * kLog2e));
       l[i] = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+      l[i] = mul2(l[i], l[i]);
       z2 = add2(z2, l[i]);
       dot2 = fma2(l[i], share[i], dot2);
     }
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
       const float2 lo = l[i / 2];
       if (kVec) {
         const float2 hi = l[i / 2 + (kVec ? 1 : 0)];
-        if (e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        if (kFull || e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
       } else {
         if (e < E) out[e] = lo.x;
         if (e + tpr < E) out[e + tpr] = lo.y;
@@ -304,26 +308,34 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
 
 // After the counting kernel the losses may start early (they wait for its
 // result); without it they follow the caller's work as any launch does.
-template <int kValues, bool kVec>
+template <int kValues, bool kVec, bool kFull>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
-  const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec>), done, 2 * operand, true);
+  const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec, kFull>), done, 2 * operand, true);
   if (err != cudaSuccess) return err;
   const size_t smem = (args.a.d_in ? 2 : 1) * operand;
-  if (args.cluster) return launch_cluster(loss_kernel<kValues, kVec>, args.cluster, kThreads, smem, stream, args);
-  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec>, grid, kThreads, smem, stream, args);
-  loss_kernel<kValues, kVec><<<grid, kThreads, smem, stream>>>(args);
+  if (args.cluster) return launch_cluster(loss_kernel<kValues, kVec, kFull>, args.cluster, kThreads, smem, stream, args);
+  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec, kFull>, grid, kThreads, smem, stream, args);
+  loss_kernel<kValues, kVec, kFull><<<grid, kThreads, smem, stream>>>(args);
   return cudaGetLastError();
 }
 
-template <bool kVec>
+template <bool kVec, bool kFull>
 cudaError_t launch_losses(const Args& args, int values, int grid, cudaStream_t stream) {
-  if (values <= 4) return launch_one<4, kVec>(args, grid, stream);
-  if (values <= 8) return launch_one<8, kVec>(args, grid, stream);
-  if (values <= 12) return launch_one<12, kVec>(args, grid, stream);
-  if (values <= 16) return launch_one<16, kVec>(args, grid, stream);
-  return launch_one<32, kVec>(args, grid, stream);
+  if (values <= 4) return launch_one<4, kVec, kFull>(args, grid, stream);
+  if (values <= 8) return launch_one<8, kVec, kFull>(args, grid, stream);
+  if (values <= 12) return launch_one<12, kVec, kFull>(args, grid, stream);
+  if (values <= 16) return launch_one<16, kVec, kFull>(args, grid, stream);
+  return launch_one<32, kVec, kFull>(args, grid, stream);
+}
+
+// A row fills all of its lanes' values where E is so many: nothing to check.
+cudaError_t launch_losses(const Args& args, bool vec, int values, int grid, cudaStream_t stream) {
+  if (!vec) return launch_losses<false, false>(args, values, grid, stream);
+  const bool full = args.a.E == args.tpr * values && (values <= 16 || values == 32);
+  return full ? launch_losses<true, true>(args, values, grid, stream)
+              : launch_losses<true, false>(args, values, grid, stream);
 }
 
 constexpr size_t kPartialBytes = kRouterLossMaxBlocks * 2 * sizeof(double);
@@ -349,7 +361,7 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   if (want <= kClusterMost * 2) {
     args.cluster = 1;
     while (args.cluster < want && args.cluster < kClusterMost) args.cluster *= 2;
-    return vec ? launch_losses<true>(args, values, 0, stream) : launch_losses<false>(args, values, 0, stream);
+    return launch_losses(args, vec, values, 0, stream);
   }
   const int64_t most = num_sms * (values <= 12 ? 3 : 2);
   const int grid = static_cast<int>(want < most ? want : most);
@@ -358,7 +370,7 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
     count_kernel<<<kCountBlocks, kThreads, 0, stream>>>(a.mask, a.T, kept);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  err = vec ? launch_losses<true>(args, values, grid, stream) : launch_losses<false>(args, values, grid, stream);
+  err = launch_losses(args, vec, values, grid, stream);
   if (err != cudaSuccess) return err;
   return launch_dependent(finish_kernel, 1, kThreads, 0, stream, args.partial, grid, a.losses);
 }
