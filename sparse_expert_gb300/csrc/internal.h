@@ -285,7 +285,7 @@ struct RouterLoss {
   float* losses;          // [2]
   void* workspace;        // router_loss_workspace_bytes()
 };
-constexpr int kRouterLossMaxBlocks = 1024;
+constexpr int kRouterLossMaxPieces = 8192;
 size_t router_loss_workspace_bytes();
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream);
 

@@ -1,5 +1,5 @@
-// Layer norm over the rows of [T, d], forward (layer_norm.cu) and backward
-// (layer_norm_backward.cu): what both share.
+// Layer norm over the rows of [T, d], forward (layer_norm_forward.cuh) and
+// backward (layer_norm_backward.cuh): what both share.
 //
 //   z  = round(x + residual)  (or x)          mu = mean z
 //   r  = 1 / sqrt(mean (z - mu)^2 + eps)      n  = (z - mu) r
@@ -37,12 +37,58 @@
 #include "launch.cuh"
 
 namespace moe {
-namespace {
 
-struct Row {
+struct NormRows {
   const void* ptr;
   int64_t stride;  // elements between rows
 };
+
+struct NormForwardArgs {
+  NormRows x, res;
+  const void* w;
+  const void* b;
+  bool w_f32;  // weight and bias are fp32, else of the rows' type
+  int64_t T;
+  int d;
+  float eps;
+  void* y;
+  void* z;
+  float* stats;
+  int tpr;
+  int tile_rounds;  // rounds of a block's piece of work
+  int64_t piece;    // its rows
+  bool steal;       // more pieces than SMs
+};
+
+struct NormBackwardArgs {
+  NormRows dy, z, dz;
+  const float* stats;
+  const void* w;
+  bool w_f32;
+  int64_t T;
+  int d;
+  void* dx;
+  float* partial;  // [blocks][2][d]: the block's sums of dy n, and of dy
+  float* dw;  // the sums over all blocks, where one cluster holds them
+  float* db;
+  bool want_w, want_b;
+  int tpr;
+  int cluster;  // blocks of that cluster, or 0: the sums go to `partial`
+};
+
+// One translation unit for each element type (layer_norm_f32.cu, _bf16.cu,
+// _f16.cu).  The backward sets *blocks to the number of partial sums it left,
+// or a.cluster where it left none.
+template <typename T>
+cudaError_t norm_forward_typed(NormForwardArgs& a, int num_sms, cudaStream_t stream);
+template <typename T>
+cudaError_t norm_backward_typed(NormBackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream);
+
+namespace {
+
+using Row = NormRows;
+using ForwardArgs = NormForwardArgs;
+using BackwardArgs = NormBackwardArgs;
 
 constexpr int kMaxWarps = 32;
 
@@ -78,8 +124,8 @@ __device__ __forceinline__ V over_warps(V v, int warps) {
 // reaches the next exchange's barrier only after it has read this one's
 // buffer, so one barrier each is enough.
 template <int kRows>
-__device__ __forceinline__ void exchange(float2 (&v)[kRows], int tpr, float2* red) {
-  const int lane = threadIdx.x & 31, warps = tpr >> 5, group = threadIdx.x / tpr;
+__device__ __forceinline__ void exchange(float2 (&v)[kRows], int tpr, int group, float2* red) {
+  const int lane = threadIdx.x & 31, warps = tpr >> 5;
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
     if (lane == i) red[i * kMaxWarps + (threadIdx.x >> 5)] = v[i];
@@ -87,21 +133,21 @@ __device__ __forceinline__ void exchange(float2 (&v)[kRows], int tpr, float2* re
 #pragma unroll
   for (int i = 0; i < kRows; ++i) v[i] = red[i * kMaxWarps + group * warps + (lane & (warps - 1))];
 }
-__device__ __forceinline__ float2 exchange(float2 v, int tpr, float2* red) {
+__device__ __forceinline__ float2 exchange(float2 v, int tpr, int group, float2* red) {
   float2 a[1] = {v};
-  exchange(a, tpr, red);
+  exchange(a, tpr, group, red);
   return a[0];
 }
 
 // Sums over the row's group, in every thread of it.
 __device__ __forceinline__ float2 group_reduce(float2 v, int tpr, float2* red) {
   v = warp_reduce(v, tpr);
-  return tpr <= 32 ? v : over_warps(exchange(v, tpr, red), tpr >> 5);
+  return tpr <= 32 ? v : over_warps(exchange(v, tpr, threadIdx.x / tpr, red), tpr >> 5);
 }
 
 __device__ __forceinline__ float group_reduce(float v, int tpr, float2* red) {
   v = warp_reduce(v, tpr);
-  return tpr <= 32 ? v : over_warps(exchange(make_float2(v, 0.0f), tpr, red).x, tpr >> 5);
+  return tpr <= 32 ? v : over_warps(exchange(make_float2(v, 0.0f), tpr, threadIdx.x / tpr, red).x, tpr >> 5);
 }
 
 template <typename T>

@@ -1,24 +1,10 @@
 // Layer norm, backward (the formulas and the forms: layer_norm.cuh).
+#pragma once
+
 #include "layer_norm.cuh"
 
 namespace moe {
 namespace {
-
-struct BackwardArgs {
-  Row dy, z, dz;
-  const float* stats;
-  const void* w;
-  bool w_f32;
-  int64_t T;
-  int d;
-  void* dx;
-  float* partial;  // [blocks][2][d]: the block's sums of dy n, and of dy
-  float* dw;  // the sums over all blocks, where one cluster holds them
-  float* db;
-  bool want_w, want_b;
-  int tpr;
-  int cluster;  // blocks of that cluster, or 0: the sums go to `partial`
-};
 
 // Rows in flight: what the SM's shared memory holds with three operands, at
 // most 432 bytes a thread.
@@ -318,26 +304,6 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const BackwardArgs a, 
   if (a.want_b) out[a.d + j] = sb;
 }
 
-// dw and db: the blocks' sums added in block order, in 32 interleaved
-// partial sums a column.
-__global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ partial, int blocks, int d,
-                                                      float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float part[32][33];
-  wait_for_previous();
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + lane;
-  float* out = blockIdx.y ? db : dw;
-  if (out == nullptr) return;
-  float s = 0.0f;
-  if (j < d)
-    for (int b = slice; b < blocks; b += 32) s += partial[(static_cast<int64_t>(b) * 2 + blockIdx.y) * d + j];
-  part[slice][lane] = s;
-  __syncthreads();
-  s = group_sum(part[lane][slice], 32);  // column `slice` of the block
-  const int col = blockIdx.x * 32 + slice;
-  if (lane == 0 && col < d) out[col] = s;
-}
-
 // ---- host
 // Blocks of the one cluster that takes T rows, or 0 where they are more than
 // 2 rounds of the largest (further rounds cost more than the second launch
@@ -369,10 +335,10 @@ cudaError_t backward_ring(BackwardArgs& a, int num_sms, int* blocks, cudaStream_
   return cudaGetLastError();
 }
 
-// The kernel made for this number of threads, where rows fill their chunks.
+// The kernel made for this number of threads.
 template <typename T, int kChunks, Fit kFit>
 cudaError_t backward_sized(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
-  if constexpr (kFit == kFull && kChunks > 1) {
+  if constexpr (kChunks > 1) {
     switch (a.tpr) {
       case 32: return backward_ring<T, kChunks, kFit, 32>(a, num_sms, blocks, stream);
       case 64: return backward_ring<T, kChunks, kFit, 64>(a, num_sms, blocks, stream);
@@ -412,8 +378,10 @@ cudaError_t backward_fit(BackwardArgs& a, int per_thread, int num_sms, int* bloc
   return backward_sized<T, 3, kFit>(a, num_sms, blocks, stream);
 }
 
+}  // namespace
+
 template <typename T>
-cudaError_t backward_typed(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
+cudaError_t norm_backward_typed(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
   constexpr int N = kChunk<T>, e = sizeof(T);
   Lie lie(a.dy.ptr, a.T > 1 ? a.dy.stride * e : a.d * e);
   lie.add(a.z.ptr, a.T > 1 ? a.z.stride * e : a.d * e);
@@ -441,29 +409,6 @@ cudaError_t backward_typed(BackwardArgs& a, int num_sms, int* blocks, cudaStream
   *blocks = static_cast<int>(a.T < 64 ? a.T : 64);
   column_sums_kernel<T><<<dim3((a.d + 255) / 256, *blocks), 256, 0, stream>>>(a, *blocks);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-size_t norm_backward_workspace_bytes(int64_t T, int d) {
-  const int64_t blocks = T < kNormMaxBlocks ? T : kNormMaxBlocks;
-  return align_up(static_cast<size_t>(blocks < 1 ? 1 : blocks) * 2 * d * 4);
-}
-
-cudaError_t launch_layer_norm_backward(const NormBackward& f, int num_sms, cudaStream_t stream) {
-  BackwardArgs a{{f.dy, f.dy_stride}, {f.z, f.z_stride}, {f.dz, f.dz_stride}, f.stats, f.weight,
-                 f.weight_dtype == MOE_F32, f.T, f.d, f.dx, f.partial, f.dweight, f.dbias, f.dweight != nullptr,
-                 f.dbias != nullptr, 0, 0};
-  int blocks = 0;
-  cudaError_t err;
-  switch (f.dtype) {
-    case MOE_F32: err = backward_typed<float>(a, num_sms, &blocks, stream); break;
-    case MOE_BF16: err = backward_typed<__nv_bfloat16>(a, num_sms, &blocks, stream); break;
-    default: err = backward_typed<__half>(a, num_sms, &blocks, stream); break;
-  }
-  if (err != cudaSuccess || a.cluster || !(a.want_w || a.want_b)) return err;
-  return launch_dependent(finish_kernel, dim3((f.d + 31) / 32, 2), 1024, 0, stream, f.partial, blocks, f.d, f.dweight,
-                          f.dbias);
 }
 
 }  // namespace moe

@@ -17,6 +17,11 @@
 // own values of the next row into its own slots of shared memory while it
 // works on this one, so no barrier is needed and the loads never pause.
 //
+// The rows are cut into pieces of a few rounds, one for each launched block,
+// and running blocks steal the launches that still wait; each piece leaves
+// its own sums, which are added in the pieces' order, so it does not matter
+// which block did it.
+//
 // The mask is counted by a kernel of its own first: every block needs N, and
 // each counting for itself (in the first version) cost more than the losses
 // (65,536 tokens: 349 us in all).  A small problem is one cluster of blocks
@@ -29,15 +34,17 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kCountBlocks = 64;
 
 struct Args {
   RouterLoss a;
   const int32_t* kept;  // [kCountBlocks] tokens kept, by the counting kernel; null without a mask
-  double* partial;      // [blocks][2], unless one cluster adds up the losses
+  float2* partial;      // [pieces]: sums of s_t and lse_t^2, unless one cluster adds them up
   int tpr;
   int cluster;          // its blocks, or 0
+  int rounds;           // of a piece
+  bool steal;
 };
 
 __device__ __forceinline__ float group_max(float v, int width) {
@@ -141,31 +148,40 @@ __device__ __forceinline__ float exp2_approx(float v) {
   return r;
 }
 
-// Rows in flight: this one and the next two where a lane has up to 12 values
-// (3 resident blocks of 74 KB), else the next one.
-template <int kValues>
-constexpr int kStages = kValues <= 12 ? 3 : 2;
+// Rows in flight a group: this one and the next two.
+constexpr int kStages = 3;
+constexpr int kStealRounds = 8;  // at least the rows in flight
 
 template <int kValues, bool kVec, bool kFull>
-__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(const Args args) {
+__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
-  constexpr int kPairsRow = kValues / 2, S = kStages<kValues>;
+  constexpr int kPairsRow = kValues / 2, S = kStages, kWarps = kThreads / 32;
   constexpr uint32_t kOperand = kValues / (kVec ? 4 : 1) * kPitch<kVec>;
   const int tpr = args.tpr, E = a.E;
   extern __shared__ uint4 ring[];  // [stage][operand][vector or value][thread]
-  __shared__ int64_t red_i[kThreads / 32];
-  __shared__ double red[kThreads / 32], block_losses[2];
+  __shared__ int64_t red_i[kWarps];
+  __shared__ float2 red[2][kWarps], block_losses;
+  __shared__ uint4 answer;
+  __shared__ uint64_t answer_bar;
+  __shared__ volatile int give_up;  // the bounded wait's other way out, unused
   let_next_start();
-  const int lane = threadIdx.x % tpr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / tpr);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr);
-  const int64_t rounds = (a.T - first + step - 1) / step;
-  int64_t t = first + threadIdx.x / tpr;
+  const int lane = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = kThreads / tpr;
+  if (args.steal && threadIdx.x == 0) {
+    give_up = 0;
+    mbar_init(&answer_bar, 1);
+    fence_barrier_init();
+    steal_request(&answer, &answer_bar);
+  }
+  // a piece: args.rounds rounds of a row a group, consecutive rows
+  const int64_t piece_rows = static_cast<int64_t>(args.rounds) * groups;
   auto kept_row = [&](int64_t row) { return row < a.T && (!a.mask || __ldg(a.mask + row) != 0); };
   // a masked row of a gradient accumulated in place is left as it is
   const bool in_place = a.d_in && a.d_in == a.d_logits;
   const uint32_t own = smem_addr(ring) + threadIdx.x * (kVec ? 16 : 4), stage_bytes = (a.d_in ? 2 : 1) * kOperand;
-  int64_t ahead = t;
+  int64_t piece = blockIdx.x, next_piece = -1;
+  int64_t ahead = piece * piece_rows + group;
+  int ahead_round = 0;
+  uint32_t answers = 0;
   bool ahead_live = kept_row(ahead);
   uint32_t live_bits = 0;  // bit k: the row k rounds after this one is kept
   auto fetch = [&](uint32_t stage, int round) {
@@ -174,7 +190,31 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
       fetch_row<kValues, kVec, kFull>(stage + kOperand, a.d_in + ahead * E, E, lane, tpr);
     asm volatile("cp.async.commit_group;" ::: "memory");
     live_bits |= static_cast<uint32_t>(ahead_live) << round;
-    ahead += step;
+    ahead += groups;
+    // after a piece's last round, on to the next piece; every thread of the
+    // block comes here in the same round
+    if (++ahead_round == args.rounds) {
+      ahead_round = 0;
+      next_piece = -1;
+      ahead = a.T;
+      if (args.steal && answers != ~0u) {
+        if (answers == 0) __syncthreads();  // the barrier is initialised
+        const bool told = mbar_wait(&answer_bar, answers & 1, &give_up);
+        const int block = told ? steal_answer(&answer) : -1;
+        // an answer that did not come in time is taken as a refusal:
+        // launches that were not cancelled start as blocks of their own
+        const bool stolen = __syncthreads_and(block >= 0);  // and all have read it
+        answers = stolen ? answers + 1 : ~0u;
+        if (stolen) {
+          if (threadIdx.x == 0) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            steal_request(&answer, &answer_bar);
+          }
+          next_piece = block;
+          ahead = next_piece * piece_rows + group;
+        }
+      }
+    }
     ahead_live = kept_row(ahead);
   };
 #pragma unroll
@@ -205,9 +245,10 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
   const float cb = a.balance_coef * static_cast<float>(E), cz = 2.0f * a.z_coef;
   constexpr float kLog2e = 1.4426950408889634f;
-  float sum_s = 0.0f, sum_z = 0.0f;
-  uint32_t stage = own, next = own + (S - 1) * stage_bytes;
-  for (int64_t round = 0; round < rounds; ++round, t += step, live_bits >>= 1) {
+  float2 sums = both(0.0f);  // of s_t and lse_t^2 over the piece
+  uint32_t stage = own, next = own + (S - 1) * stage_bytes, parity = 0;
+  int64_t t = piece * piece_rows + group;
+  for (int round = 0;; t += groups, live_bits >>= 1) {
     fetch(next, S - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
     const bool row = t < a.T, live = live_bits & 1u, write = row && (live || !in_place);
@@ -240,9 +281,7 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
     const float inv_z = empty ? 0.0f : __fdividef(1.0f, z);  // z in [1, E]
     const float s = dot * inv_z;
     const float lse = empty ? 0.0f : top + __logf(z);
-    sum_s += s;
-    sum_z += lse * lse;
-    if (!write) continue;
+    sums = add2(sums, make_float2(s, lse * lse));
     // p / N (cb (share - s) + cz lse) = e (scale_b share + scale_0)
     const float scale = inv_z * inv_n;
     const float2 scale_b = both(scale * cb), scale_0 = both(scale * (cz * lse - cb * s));
@@ -252,58 +291,79 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 3 : 2) loss_kernel(c
       l[i] = mul2(l[i], fma2(scale_b, share[i], scale_0));
       if (a.d_in) l[i] = add2(l[i], before[i]);
     }
+    if (write) {
 #pragma unroll
-    for (int i = 0; i < kValues; i += kVec ? 4 : 2) {
-      const int e = column<kVec>(i, lane, tpr);
-      const float2 lo = l[i / 2];
-      if (kVec) {
-        const float2 hi = l[i / 2 + (kVec ? 1 : 0)];
-        if (kFull || e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
-      } else {
-        if (e < E) out[e] = lo.x;
-        if (e + tpr < E) out[e + tpr] = lo.y;
+      for (int i = 0; i < kValues; i += kVec ? 4 : 2) {
+        const int e = column<kVec>(i, lane, tpr);
+        const float2 lo = l[i / 2];
+        if (kVec) {
+          const float2 hi = l[i / 2 + (kVec ? 1 : 0)];
+          if (kFull || e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+          if (e < E) out[e] = lo.x;
+          if (e + tpr < E) out[e + tpr] = lo.y;
+        }
       }
     }
-  }
-  // every lane of a group carries the row's sums: one of them counts
-  const double s = block_sum(lane == 0 ? static_cast<double>(sum_s) : 0.0, red);
-  const double z = block_sum(lane == 0 ? static_cast<double>(sum_z) : 0.0, red);
-  const double inv = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
-  if (!args.cluster) {
-    if (threadIdx.x == 0) {
-      args.partial[2 * blockIdx.x] = s * E * inv;
-      args.partial[2 * blockIdx.x + 1] = z * inv;
+    if (++round < args.rounds) continue;
+    // the piece's sums: every lane of a group carries its rows', so the
+    // groups of a warp add up, and then the warps
+    for (int s = tpr; s < 32; s <<= 1) {
+      sums.x += __shfl_xor_sync(0xffffffffu, sums.x, s);
+      sums.y += __shfl_xor_sync(0xffffffffu, sums.y, s);
     }
-    return;
+    if ((threadIdx.x & 31) == 0) red[parity][threadIdx.x >> 5] = sums;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sums = red[parity][0];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) sums = add2(sums, red[parity][i]);
+      if (args.cluster) block_losses = sums;
+      else args.partial[piece] = sums;
+    }
+    parity ^= 1;
+    if (next_piece < 0) break;
+    round = 0;
+    sums = both(0.0f);
+    piece = next_piece;
+    t = piece * piece_rows + group - groups;
   }
-  if (threadIdx.x == 0) {
-    block_losses[0] = s * E * inv;
-    block_losses[1] = z * inv;
-  }
+  if (!args.cluster) return;
   cluster_sync();
   if (cluster_rank() == 0 && threadIdx.x < 2) {
     double sum = 0.0;
-    for (int k = 0; k < args.cluster; ++k) sum += remote_f64(block_losses + threadIdx.x, k);
-    a.losses[threadIdx.x] = static_cast<float>(sum);
+    for (int k = 0; k < args.cluster; ++k) sum += remote_f32(threadIdx.x ? &block_losses.y : &block_losses.x, k);
+    a.losses[threadIdx.x] = n > 0 ? static_cast<float>(sum * (threadIdx.x ? 1 : E) / static_cast<double>(n)) : 0.0f;
   }
   cluster_sync();  // no block leaves while another reads its sums
 }
 
-__global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restrict__ partial, int blocks,
-                                                          float* __restrict__ losses) {
-  __shared__ double red[kThreads / 32];
+// The losses from the pieces' sums: in fp32 over each thread's pieces and the
+// lanes (fp64 additions are slow on this GPU), in fp64 over the warps.
+constexpr int kFinishThreads = 1024;
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const float2* __restrict__ partial, int pieces,
+                                                                const int32_t* __restrict__ kept, int64_t T, int E,
+                                                                float* __restrict__ losses) {
+  __shared__ float2 red[kFinishThreads / 32];
   wait_for_previous();
-  double s = 0.0, z = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += kThreads) {
-    s += partial[2 * b];
-    z += partial[2 * b + 1];
+  float2 sums = both(0.0f);
+  for (int b = threadIdx.x; b < pieces; b += kFinishThreads) sums = add2(sums, partial[b]);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    sums.x += __shfl_xor_sync(0xffffffffu, sums.x, s);
+    sums.y += __shfl_xor_sync(0xffffffffu, sums.y, s);
   }
-  s = block_sum(s, red);
-  z = block_sum(z, red);
-  if (threadIdx.x == 0) {
-    losses[0] = static_cast<float>(s);
-    losses[1] = static_cast<float>(z);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sums;
+  __syncthreads();
+  if (threadIdx.x >= 2) return;
+  int64_t n = T;
+  if (kept) {
+    n = 0;
+    for (int i = 0; i < kCountBlocks; ++i) n += kept[i];
   }
+  double sum = 0.0;
+  for (int i = 0; i < kFinishThreads / 32; ++i) sum += threadIdx.x ? red[i].y : red[i].x;
+  losses[threadIdx.x] = n > 0 ? static_cast<float>(sum * (threadIdx.x ? 1 : E) / static_cast<double>(n)) : 0.0f;
 }
 
 // After the counting kernel the losses may start early (they wait for its
@@ -311,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
 template <int kValues, bool kVec, bool kFull>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
+  constexpr size_t operand = kStages * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
   const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec, kFull>), done, 2 * operand, true);
   if (err != cudaSuccess) return err;
   const size_t smem = (args.a.d_in ? 2 : 1) * operand;
@@ -338,7 +398,7 @@ cudaError_t launch_losses(const Args& args, bool vec, int values, int grid, cuda
               : launch_losses<true, false>(args, values, grid, stream);
 }
 
-constexpr size_t kPartialBytes = kRouterLossMaxBlocks * 2 * sizeof(double);
+constexpr size_t kPartialBytes = kRouterLossMaxPieces * sizeof(float2);
 
 }  // namespace
 
@@ -346,7 +406,7 @@ size_t router_loss_workspace_bytes() { return align_up(kPartialBytes + kCountBlo
 
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream) {
   auto* kept = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + kPartialBytes);
-  Args args{a, nullptr, static_cast<double*>(a.workspace), 1, 0};
+  Args args{a, nullptr, static_cast<float2*>(a.workspace), 1, 0, 1, false};
   const uintptr_t low = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_in) |
                         reinterpret_cast<uintptr_t>(a.d_logits);
   const bool vec = a.E % 4 == 0 && low % 16 == 0;
@@ -361,10 +421,18 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   if (want <= kClusterMost * 2) {
     args.cluster = 1;
     while (args.cluster < want && args.cluster < kClusterMost) args.cluster *= 2;
+    args.rounds = static_cast<int>((want + args.cluster - 1) / args.cluster);
     return launch_losses(args, vec, values, 0, stream);
   }
-  const int64_t most = num_sms * (values <= 12 ? 3 : 2);
-  const int grid = static_cast<int>(want < most ? want : most);
+  const int64_t resident = num_sms * (values <= 12 ? 6 : 4);
+  int64_t rounds = (want + resident - 1) / resident;
+  if (rounds >= 2 * kStealRounds) {
+    args.steal = true;
+    rounds = (want + kRouterLossMaxPieces - 1) / kRouterLossMaxPieces;
+    if (rounds < kStealRounds) rounds = kStealRounds;
+  }
+  args.rounds = static_cast<int>(rounds);
+  const int grid = static_cast<int>((want + rounds - 1) / rounds);
   if (a.mask) {
     args.kept = kept;
     count_kernel<<<kCountBlocks, kThreads, 0, stream>>>(a.mask, a.T, kept);
@@ -372,7 +440,7 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   }
   err = launch_losses(args, vec, values, grid, stream);
   if (err != cudaSuccess) return err;
-  return launch_dependent(finish_kernel, 1, kThreads, 0, stream, args.partial, grid, a.losses);
+  return launch_dependent(finish_kernel, 1, kFinishThreads, 0, stream, args.partial, grid, args.kept, a.T, a.E, a.losses);
 }
 
 }  // namespace moe
