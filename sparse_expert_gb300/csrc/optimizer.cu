@@ -144,6 +144,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The largest of a and the magnitudes of b and c.
+__device__ __forceinline__ float max3_nan_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ float decode(uint8_t code, float scale) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
   return __fmul_rn(__half2float(__half(h)), scale);
@@ -185,6 +192,9 @@ __device__ __forceinline__ void adamw_pair(const moe_adamw_hyper_t& h, float dec
   p = fma2(change, both(-1.0f), p);
 }
 
+// Not zero if a byte of w is zero.
+__device__ __forceinline__ uint32_t has_zero_byte(uint32_t w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
+
 // E4M3 codes of eight values, four to a word.
 __device__ __forceinline__ uint2 encode8(const float2 (&x)[4], float inv) {
   uint32_t w[4];
@@ -202,42 +212,27 @@ __device__ __forceinline__ void decode8(const uint2& codes, float scale, float2 
   }
 }
 
-// A chunk of a tensor with aligned pointers: eight consecutive values a
-// thread, so sixteen lanes hold the 128 values of a scale.  The thread at the
-// tensor's end reads and writes its values one by one, those behind it none
-// (their values are zero and raise no maximum).
+// A whole chunk of a tensor with aligned pointers: eight consecutive values
+// a thread, so sixteen lanes hold the 128 values of a scale.
 template <bool kBits8>
-__device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
+__device__ __forceinline__ void adamw_whole_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
                                             int64_t begin) {
   const int64_t j = begin + threadIdx.x * 8;
-  const int count = t.n - j >= 8 ? 8 : t.n > j ? static_cast<int>(t.n - j) : 0;
-  Raw8 raw_g{}, raw_p{}, raw_m{}, raw_v{};
-  uint2 code_m = make_uint2(0, 0), code_v = make_uint2(0, 0);
-  float ms = 0.0f, vs = 0.0f;
+  Raw8 raw_g, raw_p, raw_m, raw_v;
+  uint2 code_m, code_v;
+  float ms, vs;
+  load8(t.grad, t.grad_type, j, raw_g);
   const bool master = t.master != nullptr;
   const int p_type = master ? static_cast<int>(MOE_F32) : t.param_type;
-  const void* p_in = master ? t.master : t.param;
-  if (count == 8) {
-    load8(t.grad, t.grad_type, j, raw_g);
-    load8(p_in, p_type, j, raw_p);
-    if (kBits8) {
-      code_m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
-      code_v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
-    } else {
-      load8_f32(static_cast<const float*>(t.m) + j, raw_m.w);
-      load8_f32(static_cast<const float*>(t.v) + j, raw_v.w);
-    }
-  } else {
-    load_some(t.grad, t.grad_type == MOE_F32 ? 4 : 2, j, count, raw_g.w);
-    load_some(p_in, p_type == MOE_F32 ? 4 : 2, j, count, raw_p.w);
-    load_some(t.m, kBits8 ? 1 : 4, j, count, raw_m.w);
-    load_some(t.v, kBits8 ? 1 : 4, j, count, raw_v.w);
-    code_m = make_uint2(raw_m.w[0], raw_m.w[1]);
-    code_v = make_uint2(raw_v.w[0], raw_v.w[1]);
-  }
-  if (kBits8 && count > 0) {
+  load8(master ? t.master : t.param, p_type, j, raw_p);
+  if (kBits8) {
+    code_m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
+    code_v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
     ms = t.m_scale[j / kScaleBlock];
     vs = t.v_scale[j / kScaleBlock];
+  } else {
+    load8_f32(static_cast<const float*>(t.m) + j, raw_m.w);
+    load8_f32(static_cast<const float*>(t.v) + j, raw_v.w);
   }
   const float factor = factor_p ? *factor_p : 1.0f;
   if (!isfinite(factor)) return;
@@ -256,7 +251,106 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) adamw_pair(h, decay, mul2(g[i], both(factor)), p[i], m[i], v[i], root[i]);
-  if (count == 8) {
+  if (master) store8(t.master, MOE_F32, j, p);
+  store8(t.param, t.param_type, j, p);
+  if (!kBits8) {
+    store8(t.m, MOE_F32, j, m);
+    store8(t.v, MOE_F32, j, v);
+    return;
+  }
+  float m_max = 0.0f, v_max = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m_max = max3_nan_abs(m_max, m[i].x, m[i].y);
+    v_max = max3_nan_abs(v_max, root[i].x, root[i].y);
+  }
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1) {
+    m_max = max_nan(m_max, __shfl_xor_sync(0xffffffffu, m_max, s));
+    v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, s));
+  }
+  float m_scale, m_inv, v_scale, v_inv;
+  block_scale(m_max, &m_scale, &m_inv);
+  block_scale(v_max, &v_scale, &v_inv);
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = encode8(m, m_inv);
+  uint2 codes = encode8(root, v_inv);
+  if (has_zero_byte(codes.x) | has_zero_byte(codes.y)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t& w = i < 4 ? codes.x : codes.y;
+      const uint32_t one = 1u << (8 * (i & 3));
+      if ((w & (one * 255u)) == 0 && (i & 1 ? root[i / 2].y : root[i / 2].x) > 0.0f) w |= one;
+    }
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
+  if ((threadIdx.x & 15) == 0) {
+    t.m_scale[j / kScaleBlock] = m_scale;
+    t.v_scale[j / kScaleBlock] = v_scale;
+  }
+}
+
+// The last, partial chunk of such a tensor: the thread at the tensor's end
+// reads and writes its values one by one, those behind it none (their values
+// are zero and raise no maximum).
+struct Loaded {
+  Raw8 g, p, m, v;  // m, v: with 8 bits the codes, in the first two words
+  float ms, vs;
+  int count;        // values of the eight that exist
+};
+
+template <bool kBits8>
+__device__ __forceinline__ void load_vectors(const Tensor& t, int64_t j, Loaded& x) {
+  const bool master = t.master != nullptr;
+  const int p_type = master ? static_cast<int>(MOE_F32) : t.param_type;
+  const void* p_in = master ? t.master : t.param;
+  x.ms = x.vs = 0.0f;
+  x.count = 8;
+  if (j + 8 <= t.n) {
+    load8(t.grad, t.grad_type, j, x.g);
+    load8(p_in, p_type, j, x.p);
+    if (kBits8) {
+      const uint2 m = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + j);
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + j);
+      x.m.w[0] = m.x, x.m.w[1] = m.y, x.v.w[0] = v.x, x.v.w[1] = v.y;
+    } else {
+      load8_f32(static_cast<const float*>(t.m) + j, x.m.w);
+      load8_f32(static_cast<const float*>(t.v) + j, x.v.w);
+    }
+  } else {
+    x.count = t.n > j ? static_cast<int>(t.n - j) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.g.w[i] = x.p.w[i] = x.m.w[i] = x.v.w[i] = 0;
+    load_some(t.grad, t.grad_type == MOE_F32 ? 4 : 2, j, x.count, x.g.w);
+    load_some(p_in, p_type == MOE_F32 ? 4 : 2, j, x.count, x.p.w);
+    load_some(t.m, kBits8 ? 1 : 4, j, x.count, x.m.w);
+    load_some(t.v, kBits8 ? 1 : 4, j, x.count, x.v.w);
+  }
+  if (kBits8 && x.count > 0) {
+    x.ms = t.m_scale[j / kScaleBlock];
+    x.vs = t.v_scale[j / kScaleBlock];
+  }
+}
+
+template <bool kBits8>
+__device__ __forceinline__ void step_vectors(const Tensor& t, const moe_adamw_hyper_t& h, float factor, int64_t j,
+                                             const Loaded& x) {
+  const bool master = t.master != nullptr;
+  const float decay = h.decay * t.decay;
+  float2 g[4], p[4], m[4], v[4], root[4];
+  values8(x.g, t.grad_type, g);
+  values8(x.p, master ? static_cast<int>(MOE_F32) : t.param_type, p);
+  if (kBits8) {
+    decode8(make_uint2(x.m.w[0], x.m.w[1]), x.ms, m);
+    decode8(make_uint2(x.v.w[0], x.v.w[1]), x.vs, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], v[i]);
+  } else {
+    values8(x.m, MOE_F32, m);
+    values8(x.v, MOE_F32, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) adamw_pair(h, decay, mul2(g[i], both(factor)), p[i], m[i], v[i], root[i]);
+  if (x.count == 8) {
     if (master) store8(t.master, MOE_F32, j, p);
     store8(t.param, t.param_type, j, p);
     if (!kBits8) {
@@ -266,7 +360,7 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i >= count) continue;
+      if (i >= x.count) continue;
       const float pi = i & 1 ? p[i / 2].y : p[i / 2].x;
       if (master) t.master[j + i] = pi;
       store_any(t.param, t.param_type, j + i, pi);
@@ -280,20 +374,22 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
   float m_max = 0.0f, v_max = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    m_max = max_nan(m_max, max_nan(fabsf(m[i].x), fabsf(m[i].y)));
-    v_max = max_nan(v_max, max_nan(root[i].x, root[i].y));
+    m_max = max3_nan_abs(m_max, m[i].x, m[i].y);
+    v_max = max3_nan_abs(v_max, root[i].x, root[i].y);
   }
+  // the first exchange leaves lanes 0-7 of the sixteen with maxima of m and
+  // lanes 8-15 with those of the roots; each half makes its scale and hands
+  // the other half a copy
+  const bool upper = threadIdx.x & 8;
+  float top = max_nan(upper ? v_max : m_max, __shfl_xor_sync(0xffffffffu, upper ? m_max : v_max, 8));
 #pragma unroll
-  for (int s = 8; s > 0; s >>= 1) {
-    m_max = max_nan(m_max, __shfl_xor_sync(0xffffffffu, m_max, s));
-    v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, s));
-  }
-  float m_scale, m_inv, v_scale, v_inv;
-  block_scale(m_max, &m_scale, &m_inv);
-  block_scale(v_max, &v_scale, &v_inv);
-  const uint2 m_codes = encode8(m, m_inv);
-  uint2 codes = encode8(root, v_inv);
-  if (__vcmpeq4(codes.x, 0) | __vcmpeq4(codes.y, 0)) {
+  for (int s = 4; s > 0; s >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
+  float scale, inv;
+  block_scale(top, &scale, &inv);
+  const float other = __shfl_xor_sync(0xffffffffu, inv, 8);
+  const uint2 m_codes = encode8(m, upper ? other : inv);
+  uint2 codes = encode8(root, upper ? inv : other);
+  if (has_zero_byte(codes.x) | has_zero_byte(codes.y)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t& w = i < 4 ? codes.x : codes.y;
@@ -301,21 +397,32 @@ __device__ __forceinline__ void adamw_chunk(const Tensor& t, const moe_adamw_hyp
       if ((w & (one * 255u)) == 0 && (i & 1 ? root[i / 2].y : root[i / 2].x) > 0.0f) w |= one;
     }
   }
-  if (count == 8) {
+  if (x.count == 8) {
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + j) = m_codes;
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + j) = codes;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i >= count) continue;
+      if (i >= x.count) continue;
       static_cast<uint8_t*>(t.m)[j + i] = static_cast<uint8_t>((i < 4 ? m_codes.x : m_codes.y) >> (8 * (i & 3)));
       static_cast<uint8_t*>(t.v)[j + i] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
     }
   }
-  if ((threadIdx.x & 15) == 0 && count > 0) {
-    t.m_scale[j / kScaleBlock] = m_scale;
-    t.v_scale[j / kScaleBlock] = v_scale;
-  }
+  // lane 0 of the sixteen writes m's scale, lane 8 the roots' (their block
+  // exists where its first value does)
+  const int64_t block = j / kScaleBlock;
+  if ((threadIdx.x & 7) == 0 && block * kScaleBlock < t.n) (upper ? t.v_scale : t.m_scale)[block] = scale;
+}
+
+template <bool kBits8>
+__device__ __forceinline__ void adamw_last_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
+                                                 int64_t begin) {
+  const int64_t j = begin + threadIdx.x * 8;
+  Loaded x;
+  load_vectors<kBits8>(t, j, x);
+  const float factor = factor_p ? *factor_p : 1.0f;
+  if (!isfinite(factor)) return;
+  step_vectors<kBits8>(t, h, factor, j, x);
 }
 
 // A chunk of a tensor whose pointers are not all at 32-byte boundaries: a warp takes blocks of 128 values, lane + 32 i of each.
@@ -384,15 +491,28 @@ __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_ad
   }
 }
 
-template <int kCapacity>
-__global__ void __launch_bounds__(kBlockThreads) adamw_kernel(const __grid_constant__ List<kCapacity> list) {
+// kBits8: some tensor of the list has 8-bit states.  Those steps are bound by
+// the latency of their small loads and take 6 blocks an SM (40 registers):
+// 202M bf16 weights without masters 392 us against 462 with 5 blocks; steps
+// with 32-bit states are bound by memory and faster with 5 (201M weights with
+// masters 798 us, 856 with 6).
+template <int kCapacity, bool kBits8>
+__global__ void __launch_bounds__(kBlockThreads, kBits8 ? 6 : 5)
+    adamw_kernel(const __grid_constant__ List<kCapacity> list) {
   const moe_adamw_hyper_t h = list.hyper_dev ? *list.hyper_dev : list.hyper;
   const int which = tensor_of(list, blockIdx.x);
   const Tensor& t = list.t[which];
   const int64_t begin = static_cast<int64_t>(blockIdx.x - list.first[which]) * kChunkValues;
-  if (!t.vec) adamw_scalar_chunk(t, h, list.grad_scale, begin);
-  else if (t.bits8) adamw_chunk<true>(t, h, list.grad_scale, begin);
-  else adamw_chunk<false>(t, h, list.grad_scale, begin);
+  const bool whole = begin + kChunkValues <= t.n;
+  if (!t.vec) {
+    adamw_scalar_chunk(t, h, list.grad_scale, begin);
+  } else if (kBits8 && t.bits8) {
+    if (whole) adamw_whole_chunk<true>(t, h, list.grad_scale, begin);
+    else adamw_last_chunk<true>(t, h, list.grad_scale, begin);
+  } else {
+    if (whole) adamw_whole_chunk<false>(t, h, list.grad_scale, begin);
+    else adamw_last_chunk<false>(t, h, list.grad_scale, begin);
+  }
 }
 
 // ---- gradient norm
@@ -536,7 +656,10 @@ cudaError_t adamw_all(const moe_adamw_tensor_t* tensors, int n_tensors, const mo
   list.grad_scale = grad_scale;
   for (int at = 0; at < n_tensors;) {
     if (fill(list, tensors, n_tensors, 0, &at) == 0) continue;
-    adamw_kernel<kCapacity><<<list.chunks, kBlockThreads, 0, stream>>>(list);
+    bool bits8 = false;
+    for (int i = 0; i < list.count; ++i) bits8 |= list.t[i].bits8 != 0;
+    if (bits8) adamw_kernel<kCapacity, true><<<list.chunks, kBlockThreads, 0, stream>>>(list);
+    else adamw_kernel<kCapacity, false><<<list.chunks, kBlockThreads, 0, stream>>>(list);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }

@@ -148,14 +148,16 @@ __device__ __forceinline__ float exp2_approx(float v) {
   return r;
 }
 
-// Rows in flight a group: this one and the next two.
-constexpr int kStages = 3;
+// Rows in flight a group: this one and the next two, or the next one where a
+// lane has more than 16 values.
+template <int kValues>
+constexpr int kStages = kValues <= 16 ? 3 : 2;
 constexpr int kStealRounds = 8;  // at least the rows in flight
 
 template <int kValues, bool kVec, bool kFull>
 __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
-  constexpr int kPairsRow = kValues / 2, S = kStages, kWarps = kThreads / 32;
+  constexpr int kPairsRow = kValues / 2, S = kStages<kValues>, kWarps = kThreads / 32;
   constexpr uint32_t kOperand = kValues / (kVec ? 4 : 1) * kPitch<kVec>;
   const int tpr = args.tpr, E = a.E;
   extern __shared__ uint4 ring[];  // [stage][operand][vector or value][thread]
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const float2* __
 template <int kValues, bool kVec, bool kFull>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr size_t operand = kStages * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
+  constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
   const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec, kFull>), done, 2 * operand, true);
   if (err != cudaSuccess) return err;
   const size_t smem = (args.a.d_in ? 2 : 1) * operand;
@@ -410,7 +412,11 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   const uintptr_t low = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.d_in) |
                         reinterpret_cast<uintptr_t>(a.d_logits);
   const bool vec = a.E % 4 == 0 && low % 16 == 0;
-  const int units = vec ? a.E / 4 : a.E, per = vec ? 1 : 4;
+  // few lanes with up to 12 values each (16 single ones): a row's reductions
+  // cost as much as a dozen values of every lane that takes part (60,000 x 64
+  // with 4, 12 and 16 values a lane: 16.6, 13.9 and 16.1 us; 65,536 x 384 with
+  // 12 and 24: 60.7 and 63.3 us)
+  const int units = vec ? a.E / 4 : a.E, per = vec ? 3 : 16;
   while (args.tpr < 32 && args.tpr * per < units) args.tpr *= 2;
   const int values = (units + args.tpr - 1) / args.tpr * (vec ? 4 : 1);
   const int groups = kThreads / args.tpr;
