@@ -11,7 +11,7 @@
 // once.  A row belongs to a group of `tpr` threads (a power of two), and
 // groups walk over the rows.  Three forms, by what the rows allow:
 //   - rings of 16-byte chunks, where all operands of a row lie alike within
-//     16 bytes (contiguous tensors of any d do) and 3 chunks a thread of 512
+//     16 bytes (contiguous tensors of any d do) and 4 chunks a thread of 512
 //     hold a row: thread i of a group owns the aligned chunks i, i + tpr, ...
 //     of its rows; it copies its own chunks of the coming rows into its own
 //     slots of shared memory asynchronously, several rows ahead, and reads
@@ -24,12 +24,15 @@
 //     last chunk of such a row are partial, and their other values masked.
 //   - single values (operands that lie differently): thread i owns columns
 //     i, i + tpr, ... in registers, so a warp reads neighbouring values.
-//   - rows longer than that: sweeps over the row, the later ones out of L2.
+//   - rows longer than that: a block a row that keeps the row in shared
+//     memory where it fits (else the later sweeps read it again).
 // The variance is taken from the deviations from the mean, never as a
 // difference of two sums, so a large common offset costs no digits.  Sums
 // are fp32 per thread and then trees over lanes and warps, always in the same
 // order.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -252,6 +255,36 @@ struct Place {
   }
 };
 
+// ---- long rows: units of a chunk (kVec) or of one value
+template <typename T, bool kVec>
+struct Unit {
+  static constexpr int N = kVec ? kChunk<T> : 1;
+  using Store = typename std::conditional<kVec, uint4, T>::type;
+  __device__ static __forceinline__ void values(const Store& u, float* v) {
+    if constexpr (kVec) unpack_chunk<T>(u, v);
+    else v[0] = to_f32(u);
+  }
+  __device__ static __forceinline__ Store store(const float* v) {
+    if constexpr (kVec) return pack_chunk<T>(v);
+    else return from_f32<T>(v[0]);
+  }
+  __device__ static __forceinline__ void params(const void* p, bool f32, float missing, int u, float* v) {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = missing;
+    } else if constexpr (!kVec) {
+      v[0] = param_at<T>(p, f32, u);
+    } else if (f32) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4*>(v + i) = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + u * N + i));
+    } else {
+      unpack_chunk<T>(__ldg(static_cast<const uint4*>(p) + u), v);
+    }
+  }
+};
+constexpr size_t kLongCache = 200 * 1024;  // shared memory for a long row
+
 template <typename T>
 __device__ __forceinline__ int row_offset(const Row& rows, int64_t t) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(rows.ptr) + t * rows.stride) & 15) /
@@ -301,13 +334,15 @@ struct Lie {
 
 bool param_on_chunks(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Threads for a ring's row, or 0 where 3 chunks a thread do not hold it.  A
+// Threads for a ring's row, or 0 where 4 chunks a thread do not hold it (4 for
+// the longest rows only: their registers spill a little).  A
 // row that does not start on a chunk may touch one more than it fills, and
 // has at least 8 threads (its groups' column sums are added one by one).
 int ring_threads(int d, int values, bool aligned, int* per_thread) {
   const int chunks = (d + values - 1) / values + (aligned ? 0 : 1);
   int tpr = threads_per_row(chunks, 3);
   if (!aligned && tpr < 8) tpr = 8;
+  if (tpr > kRingThreads && chunks <= 4 * kRingThreads) tpr = kRingThreads;
   *per_thread = (chunks + tpr - 1) / tpr;
   return tpr <= kRingThreads ? tpr : 0;
 }

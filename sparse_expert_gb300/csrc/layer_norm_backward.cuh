@@ -10,7 +10,7 @@ namespace {
 // most 432 bytes a thread.
 constexpr uint32_t kPitch = kRingThreads * 16;  // bytes between a thread's slots
 template <int kChunks>
-constexpr int kBackwardStages = kChunks == 1 ? 8 : kChunks == 2 ? 4 : 3;
+constexpr int kBackwardStages = kChunks == 1 ? 8 : kChunks == 2 ? 4 : kChunks == 3 ? 3 : 2;
 
 // The block's column sums from its threads': where the lanes of a warp own
 // the same columns (`same`: tpr below 32, rows that start alike) they add by
@@ -260,48 +260,86 @@ __global__ void __launch_bounds__(512) backward_values_kernel(const BackwardArgs
   if (a.cluster) finish_cluster(a, true, shared);
 }
 
-// Rows too long for the registers: dx by a block a row in two sweeps, and
-// the column sums by a block for each 256 columns and slice of rows.
-template <typename T>
-__global__ void __launch_bounds__(1024) backward_long_kernel(const BackwardArgs a) {
+// Rows too long for the registers: dx by a block a row, which keeps dy and z
+// in shared memory between its two sweeps (`cached`), and the column sums by a
+// block for each run of columns and slice of rows.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(1024) backward_long_kernel(const BackwardArgs a, bool cached) {
+  using U = Unit<T, kVec>;
+  using Store = typename U::Store;
+  extern __shared__ uint4 row_cache[];
   __shared__ float2 red[kMaxWarps];
   const int64_t t = blockIdx.x;
-  const T* dy = static_cast<const T*>(a.dy.ptr) + t * a.dy.stride;
-  const T* z = static_cast<const T*>(a.z.ptr) + t * a.z.stride;
+  const int units = a.d / U::N;
+  const Store* dy = reinterpret_cast<const Store*>(static_cast<const T*>(a.dy.ptr) + t * a.dy.stride);
+  const Store* z = reinterpret_cast<const Store*>(static_cast<const T*>(a.z.ptr) + t * a.z.stride);
+  const Store* dz = reinterpret_cast<const Store*>(static_cast<const T*>(a.dz.ptr) + (a.dz.ptr ? t * a.dz.stride : 0));
+  Store* dx = reinterpret_cast<Store*>(static_cast<T*>(a.dx) + t * a.d);
+  Store* cache = reinterpret_cast<Store*>(row_cache);
   const float mu = a.stats[t], r = a.stats[a.T + t];
+  float g[U::N], n[U::N], p[U::N];
   float2 s = make_float2(0.0f, 0.0f);
-  for (int j = threadIdx.x; j < a.d; j += blockDim.x) {
-    const float g = to_f32(dy[j]) * (a.w ? param_at<T>(a.w, a.w_f32, j) : 1.0f);
-    s.x += g;
-    s.y += g * ((to_f32(z[j]) - mu) * r);
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    const Store raw_g = dy[u], raw_n = z[u];
+    if (cached) cache[u] = raw_g, cache[units + u] = raw_n;
+    U::values(raw_g, g);
+    U::values(raw_n, n);
+    U::params(a.w, a.w_f32, 1.0f, u, p);
+#pragma unroll
+    for (int i = 0; i < U::N; ++i) {
+      s.x += g[i] * p[i];
+      s.y += g[i] * p[i] * ((n[i] - mu) * r);
+    }
   }
+  // each thread reads back only what it has written itself
+  const Store* dy_in = cached ? cache : dy;
+  const Store* z_in = cached ? cache + units : z;
   s = group_reduce(s, blockDim.x, red);
   s.x /= static_cast<float>(a.d);
   s.y /= static_cast<float>(a.d);
-  for (int j = threadIdx.x; j < a.d; j += blockDim.x) {
-    const float n = (to_f32(z[j]) - mu) * r;
-    float v = (to_f32(dy[j]) * (a.w ? param_at<T>(a.w, a.w_f32, j) : 1.0f) - s.x - n * s.y) * r;
-    if (a.dz.ptr) v += to_f32(static_cast<const T*>(a.dz.ptr)[t * a.dz.stride + j]);
-    static_cast<T*>(a.dx)[t * a.d + j] = from_f32<T>(v);
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    U::values(dy_in[u], g);
+    U::values(z_in[u], n);
+    U::params(a.w, a.w_f32, 1.0f, u, p);
+#pragma unroll
+    for (int i = 0; i < U::N; ++i) g[i] = (g[i] * p[i] - s.x - (n[i] - mu) * r * s.y) * r;
+    if (a.dz.ptr) {
+      U::values(dz[u], p);
+#pragma unroll
+      for (int i = 0; i < U::N; ++i) g[i] += p[i];
+    }
+    dx[u] = U::store(g);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) column_sums_kernel(const BackwardArgs a, int slices) {
+constexpr int kColumnThreads = 128;
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kColumnThreads) column_sums_kernel(const BackwardArgs a, int slices) {
+  using U = Unit<T, kVec>;
+  using Store = typename U::Store;
   let_next_start();
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= a.d) return;
-  float sw = 0.0f, sb = 0.0f;
+  const int u = blockIdx.x * kColumnThreads + threadIdx.x;
+  if (u >= a.d / U::N) return;
+  float sw[U::N], sb[U::N], g[U::N], n[U::N];
+#pragma unroll
+  for (int i = 0; i < U::N; ++i) sw[i] = sb[i] = 0.0f;
+#pragma unroll 4
   for (int64_t t = blockIdx.y; t < a.T; t += slices) {
-    const float g = to_f32(static_cast<const T*>(a.dy.ptr)[t * a.dy.stride + j]);
-    const float n = (to_f32(static_cast<const T*>(a.z.ptr)[t * a.z.stride + j]) - __ldg(a.stats + t)) *
-                    __ldg(a.stats + a.T + t);
-    sw += g * n;
-    sb += g;
+    U::values(reinterpret_cast<const Store*>(static_cast<const T*>(a.dy.ptr) + t * a.dy.stride)[u], g);
+    U::values(reinterpret_cast<const Store*>(static_cast<const T*>(a.z.ptr) + t * a.z.stride)[u], n);
+    const float mu = __ldg(a.stats + t), r = __ldg(a.stats + a.T + t);
+#pragma unroll
+    for (int i = 0; i < U::N; ++i) {
+      sw[i] += g[i] * ((n[i] - mu) * r);
+      sb[i] += g[i];
+    }
   }
-  float* out = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.d;
-  if (a.want_w) out[j] = sw;
-  if (a.want_b) out[a.d + j] = sb;
+  float* out = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.d + u * U::N;
+#pragma unroll
+  for (int i = 0; i < U::N; ++i) {
+    if (a.want_w) out[i] = sw[i];
+    if (a.want_b) out[a.d + i] = sb[i];
+  }
 }
 
 // ---- host
@@ -338,7 +376,9 @@ cudaError_t backward_ring(BackwardArgs& a, int num_sms, int* blocks, cudaStream_
 // The kernel made for this number of threads.
 template <typename T, int kChunks, Fit kFit>
 cudaError_t backward_sized(BackwardArgs& a, int num_sms, int* blocks, cudaStream_t stream) {
-  if constexpr (kChunks > 1) {
+  if constexpr (kChunks == 4) {
+    return backward_ring<T, kChunks, kFit, 512>(a, num_sms, blocks, stream);
+  } else if constexpr (kChunks > 1) {
     switch (a.tpr) {
       case 32: return backward_ring<T, kChunks, kFit, 32>(a, num_sms, blocks, stream);
       case 64: return backward_ring<T, kChunks, kFit, 64>(a, num_sms, blocks, stream);
@@ -371,11 +411,30 @@ cudaError_t backward_values(BackwardArgs& a, int num_sms, int* blocks, cudaStrea
   return cudaGetLastError();
 }
 
+template <typename T, bool kVec>
+cudaError_t backward_long(const BackwardArgs& a, int* blocks, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = backward_long_kernel<T, kVec>;
+  cudaError_t err = allow(reinterpret_cast<const void*>(kernel), done, kLongCache, false);
+  if (err != cudaSuccess) return err;
+  const size_t bytes = static_cast<size_t>(a.d) * sizeof(T) * 2;
+  const bool cached = bytes <= kLongCache;
+  kernel<<<static_cast<unsigned>(a.T), 1024, cached ? bytes : 0, stream>>>(a, cached);
+  err = cudaGetLastError();
+  if (err != cudaSuccess || !(a.want_w || a.want_b)) return err;
+  *blocks = static_cast<int>(a.T < 64 ? a.T : 64);
+  const int units = a.d / Unit<T, kVec>::N;
+  column_sums_kernel<T, kVec>
+      <<<dim3((units + kColumnThreads - 1) / kColumnThreads, *blocks), kColumnThreads, 0, stream>>>(a, *blocks);
+  return cudaGetLastError();
+}
+
 template <typename T, Fit kFit>
 cudaError_t backward_fit(BackwardArgs& a, int per_thread, int num_sms, int* blocks, cudaStream_t stream) {
   if (per_thread == 1) return backward_sized<T, 1, kFit>(a, num_sms, blocks, stream);
   if (per_thread == 2) return backward_sized<T, 2, kFit>(a, num_sms, blocks, stream);
-  return backward_sized<T, 3, kFit>(a, num_sms, blocks, stream);
+  if (per_thread == 3) return backward_sized<T, 3, kFit>(a, num_sms, blocks, stream);
+  return backward_sized<T, 4, kFit>(a, num_sms, blocks, stream);
 }
 
 }  // namespace
@@ -403,12 +462,7 @@ cudaError_t norm_backward_typed(BackwardArgs& a, int num_sms, int* blocks, cudaS
     if (values <= 8) return backward_values<T, 8>(a, num_sms, blocks, stream);
     return backward_values<T, 16>(a, num_sms, blocks, stream);
   }
-  backward_long_kernel<T><<<static_cast<unsigned>(a.T), 1024, 0, stream>>>(a);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || !(a.want_w || a.want_b)) return err;
-  *blocks = static_cast<int>(a.T < 64 ? a.T : 64);
-  column_sums_kernel<T><<<dim3((a.d + 255) / 256, *blocks), 256, 0, stream>>>(a, *blocks);
-  return cudaGetLastError();
+  return aligned ? backward_long<T, true>(a, blocks, stream) : backward_long<T, false>(a, blocks, stream);
 }
 
 }  // namespace moe
