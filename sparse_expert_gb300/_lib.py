@@ -9,7 +9,9 @@ is missing, importing this module fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -773,6 +775,7 @@ def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None,
     return (out, stats) if residual is None else (out, stats, z)
 
 
+@functools.lru_cache(maxsize=256)
 def moe_layer_norm_backward_workspace_bytes(T, d) -> int:
     return lib.moe_layer_norm_backward_workspace_bytes(T, d)
 
@@ -815,7 +818,7 @@ def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads
     if db is not None:
         db_ptr = db.data_ptr()
     if workspace is None:
-        size = lib.moe_layer_norm_backward_workspace_bytes(T, d)
+        size = moe_layer_norm_backward_workspace_bytes(T, d)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         size = workspace.numel()
@@ -890,28 +893,40 @@ class TensorList:
         return len(self.records)
 
 
-def _flat(t, name, dtypes, n=None, device=None):
+def _flat(t, name, dtypes, n, index):
+    """Address of a contiguous CUDA tensor of n values (any number if None) on device `index`."""
+    if t.dtype in dtypes and (n is None or t.numel() == n) and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} values, got {t.numel()}")
-    return t
+    raise ValueError(f"{name} must have {n} values, got {t.numel()}")
+
+
+_RECORD = struct.Struct("@7Qq3if")  # moe_adamw_tensor_t
+assert _RECORD.size == ctypes.sizeof(AdamWTensor)
+_F32 = (torch.float32,)
+_STATES = (torch.float32, torch.uint8)
+
+
+def _device_index(t):
+    return t.get_device() if t.is_cuda else -2  # which no tensor's device is
 
 
 def moe_tensor_list(grads) -> TensorList:
     """The list of gradients (contiguous, fp32, bf16 or fp16) for moe_grad_norm."""
     grads = list(grads)
-    records = (AdamWTensor * len(grads))()
-    for r, g in zip(records, grads):
-        _flat(g, "a gradient", _DTYPES, None, grads[0].device)
-        r.grad, r.n, r.grad_type = g.data_ptr(), g.numel(), _DTYPES[g.dtype]
-    return TensorList(records, grads, grads[0].device if grads else None, False)
+    buf = bytearray(_RECORD.size * len(grads))
+    index = _device_index(grads[0]) if grads else None
+    for i, g in enumerate(grads):
+        _RECORD.pack_into(buf, i * _RECORD.size, 0, 0, _flat(g, "a gradient", _DTYPES, None, index), 0, 0, 0, 0,
+                          g.numel(), 0, _DTYPES[g.dtype], 0, 0.0)
+    return TensorList((AdamWTensor * len(grads)).from_buffer(buf), grads, grads[0].device if grads else None, False)
 
 
 def moe_adamw_state(params, bits=32):
@@ -944,26 +959,28 @@ def moe_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, masters=No
     every = (params, grads, m, v, m_scales, v_scales, masters, decay)
     if any(len(a) != n_tensors for a in every):
         raise ValueError("the lists must have one entry for each parameter")
-    records = (AdamWTensor * n_tensors)()
-    device = params[0].device if n_tensors else None
-    for r, p, g, mm, vv, ms, vs, master, wd in zip(records, *every):
-        _flat(p, "a parameter", _DTYPES, None, device)
+    buf = bytearray(_RECORD.size * n_tensors)
+    index = _device_index(params[0]) if n_tensors else None
+    at = 0
+    for p, g, mm, vv, ms, vs, master, wd in zip(*every):
+        p_ptr = _flat(p, "a parameter", _DTYPES, None, index)
         n = p.numel()
-        _flat(g, "a gradient", _DTYPES, n, device)
-        _flat(mm, "m", (torch.float32, torch.uint8), n, device)
-        _flat(vv, "v", (mm.dtype,), n, device)
-        r.param, r.grad, r.m, r.v, r.n = p.data_ptr(), g.data_ptr(), mm.data_ptr(), vv.data_ptr(), n
-        r.param_type, r.grad_type = _DTYPES[p.dtype], _DTYPES[g.dtype]
-        r.state_bits = 32 if mm.dtype == torch.float32 else 8
-        if r.state_bits == 8:
+        g_ptr = _flat(g, "a gradient", _DTYPES, n, index)
+        m_ptr = _flat(mm, "m", _STATES, n, index)
+        v_ptr = _flat(vv, "v", (mm.dtype,), n, index)
+        bits, ms_ptr, vs_ptr, master_ptr = 32, 0, 0, 0
+        if mm.dtype is torch.uint8:
             if ms is None or vs is None:
                 raise ValueError("8-bit states need m_scales and v_scales")
-            r.m_scale = _flat(ms, "m_scales", (torch.float32,), -(-n // 128), device).data_ptr()
-            r.v_scale = _flat(vs, "v_scales", (torch.float32,), -(-n // 128), device).data_ptr()
+            bits = 8
+            ms_ptr = _flat(ms, "m_scales", _F32, -(-n // 128), index)
+            vs_ptr = _flat(vs, "v_scales", _F32, -(-n // 128), index)
         if master is not None:
-            r.master = _flat(master, "a master", (torch.float32,), n, device).data_ptr()
-        r.decay = wd
-    return TensorList(records, every, device, True)
+            master_ptr = _flat(master, "a master", _F32, n, index)
+        _RECORD.pack_into(buf, at, p_ptr, master_ptr, g_ptr, m_ptr, v_ptr, ms_ptr, vs_ptr, n, _DTYPES[p.dtype],
+                          _DTYPES[g.dtype], bits, wd)
+        at += _RECORD.size
+    return TensorList((AdamWTensor * n_tensors).from_buffer(buf), every, params[0].device if n_tensors else None, True)
 
 
 def moe_grad_norm(tensors, max_norm=float("inf"), out=None, workspace=None, stream=None):
