@@ -290,7 +290,7 @@ size_t router_loss_workspace_bytes();
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream);
 
 // The optimizer's lists of tensors (arrays in host memory).
-constexpr int kGradNormMaxBlocks = 2048;
+constexpr int kGradNormMaxBlocks = 4096;
 size_t grad_norm_workspace_bytes();
 cudaError_t launch_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out,
                              double* partial, int num_sms, cudaStream_t stream);

@@ -25,11 +25,13 @@ namespace moe {
 namespace {
 
 constexpr int kBlockThreads = 256;
-constexpr int kClusterThreads = 1024;  // of a block of the gradient norm's one cluster
 constexpr int kScaleBlock = 128;
-constexpr int kChunkValues = kBlockThreads * 8;       // one vector a thread
-constexpr int kClusterRounds = 2;                     // chunks of a block of the gradient norm's one cluster
-constexpr int kNormVectors = 4;                  // 32-byte vectors a thread of the gradient norm's chunk
+constexpr int kChunkValues = kBlockThreads * 8;  // one vector a thread
+// of the gradient norm:
+constexpr int kNormVectors = 4;        // 32-byte vectors a thread of a chunk
+constexpr int kLongShare = 24;         // chunks a resident block beyond which there are more blocks
+constexpr int kClusterThreads = 1024;  // of a block of the one cluster for small lists,
+constexpr int kClusterRounds = 2;      // and its chunks a block
 constexpr float kE4M3Max = 448.0f;
 constexpr float kTinyBlock = 7.888609052210118e-31f;  // 2^-100
 
@@ -534,10 +536,16 @@ __device__ __forceinline__ void write_norm(double squares, float max_norm, float
   out[1] = !isfinite(out[0]) ? nanf("") : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.0f;
 }
 
-// A block takes chunks blockIdx.x, + gridDim.x, ... of kNormVectors 32-byte
-// vectors a thread; the vectors of a tensor start at its first 32-byte
-// boundary, and the values before it go with the first chunk.
-// As one cluster (`out` given), its first block writes the result.
+// The squares of all gradients: one reading of them, bound by memory. A block
+// takes chunks blockIdx.x, + gridDim.x, ... of kNormVectors 32-byte vectors a
+// thread, all loads of a chunk in flight before its first use; the vectors of
+// a tensor start at its first 32-byte boundary, and the values before it go
+// with the first chunk. Up to kLongShare chunks a resident block, the blocks
+// are those that the SMs hold at once (62M bf16 values 23.4 us); beyond, they
+// are as many as there is room for partial sums, taken by the SMs as they get
+// free (403M bf16 values 115 us = 7.0 TB/s, with resident blocks alone 120).
+// A thread adds in fp32, threads and blocks in fp64, in a fixed order. As one
+// cluster (`out` given), its first block writes the result.
 template <int kCapacity, int kThreads>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ List<kCapacity> list,
                                                            double* __restrict__ partial, float max_norm, float* out) {
@@ -672,8 +680,7 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
   static std::atomic<uint64_t> done{0};
   List<kCapacity> list{};
   const int launches = (n_tensors + kCapacity - 1) / kCapacity;
-  int most = num_sms * 5;
-  if (launches > 0 && most > kGradNormMaxBlocks / launches) most = kGradNormMaxBlocks / launches;
+  const int most = launches > 0 ? kGradNormMaxBlocks / launches : 1;
   if (most < 1) return cudaErrorInvalidValue;
   int blocks = 0;
   if (launches == 1) {
@@ -691,9 +698,12 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
   for (int at = 0; at < n_tensors;) {
     const int chunks = fill(list, tensors, n_tensors, kBlockThreads, &at);
     if (chunks == 0) continue;
-    const int grid = chunks < most ? chunks : most;
+    const int resident = num_sms * 5;
+    const int shares = most > resident && chunks / resident < kLongShare ? resident : most;
+    const int grid = chunks < shares ? chunks : shares;
     if (blocks + grid > kGradNormMaxBlocks) return cudaErrorInvalidValue;
-    squares_kernel<kCapacity, kBlockThreads><<<grid, kBlockThreads, 0, stream>>>(list, partial + blocks, max_norm, nullptr);
+    squares_kernel<kCapacity, kBlockThreads>
+        <<<grid, kBlockThreads, 0, stream>>>(list, partial + blocks, max_norm, nullptr);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     blocks += grid;
