@@ -663,7 +663,7 @@ MOE_API moe_status_t moe_layer_norm_backward(const void* dy, int64_t dy_stride, 
  * A logit of -infinity takes its expert out for that token; a token whose
  * every logit is -infinity counts in N and contributes zero.  No token kept:
  * losses and gradient are zero.  Softmax statistics and sums are fp32, the
- * last sums of the losses fp64.
+ * last few sums of the losses (over a kernel's warps) fp64.
  * Workspace: moe_router_loss_workspace_bytes() bytes.
  * Supported: 1 <= E <= 1024, 0 <= T, T*E < 2^40.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
