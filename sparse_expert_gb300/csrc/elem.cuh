@@ -144,15 +144,10 @@ __device__ __forceinline__ uint4 add_chunks(const uint4& a, const uint4& b) {
   return make_uint4(add_word<T>(a.x, b.x), add_word<T>(a.y, b.y), add_word<T>(a.z, b.z), add_word<T>(a.w, b.w));
 }
 
-// Sum over the aligned group of `width` (a power of two up to 32) lanes that
-// the calling lane belongs to, the same value on each.
-__device__ __forceinline__ float group_sum(float v, int width) {
-  if (width == 32) {
+// Sum over the warp, the same value on every lane.
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  } else {
-    for (int s = width >> 1; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  }
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
 

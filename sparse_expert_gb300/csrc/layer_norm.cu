@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(1024) finish_kernel(const float* __restrict__ 
     for (int b = slice; b < blocks; b += 32) s += partial[(static_cast<int64_t>(b) * 2 + blockIdx.y) * d + j];
   part[slice][lane] = s;
   __syncthreads();
-  s = group_sum(part[lane][slice], 32);  // column `slice` of the block
+  s = warp_sum(part[lane][slice]);  // column `slice` of the block
   const int col = blockIdx.x * 32 + slice;
   if (lane == 0 && col < d) out[col] = s;
 }

@@ -29,8 +29,8 @@
 //
 // Bound by instructions and their latency together: about 36 instructions a
 // value at half the SMs' issue slots, 55 % of the memory's rate (65,536 x 384
-// added to a gradient: 55 us for the losses' kernel, 61 with the count and
-// the last sums; reading and writing alone 43).
+// added to a gradient: 58 us with the last sums and 60 with a mask, of which
+// reading and writing alone are 45).
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -58,6 +58,19 @@ __device__ __forceinline__ float group_max(float v, int width) {
     for (int s = 16; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
   } else {
     for (int s = width >> 1; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
+  }
+  return v;
+}
+
+// Two sums over a group's lanes, their exchanges side by side.
+__device__ __forceinline__ float2 group_sums(float2 v, int width) {
+  if (width == 32) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+      v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, s), __shfl_xor_sync(0xffffffffu, v.y, s)));
+  } else {
+    for (int s = width >> 1; s > 0; s >>= 1)
+      v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, s), __shfl_xor_sync(0xffffffffu, v.y, s)));
   }
   return v;
 }
@@ -159,12 +172,13 @@ template <int kValues>
 constexpr int kStages = kValues <= 16 ? 3 : 2;
 constexpr int kStealRounds = 8;  // at least the rows in flight
 
-template <int kValues, bool kVec, bool kFull>
+// kTpr: the lanes of a row where that is known when compiling, or 0.
+template <int kValues, bool kVec, bool kFull, int kTpr>
 __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
   constexpr int kPairsRow = kValues / 2, S = kStages<kValues>, kWarps = kThreads / 32;
   constexpr uint32_t kOperand = kValues / (kVec ? 4 : 1) * kPitch<kVec>;
-  const int tpr = args.tpr, E = a.E;
+  const int tpr = kTpr ? kTpr : args.tpr, E = kFull && kTpr ? kValues * kTpr : a.E;
   extern __shared__ uint4 ring[];  // [stage][operand][vector or value][thread]
   __shared__ int64_t red_i[kWarps];
   __shared__ float2 red[2][kWarps], block_losses;
@@ -283,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(c
       z2 = add2(z2, l[i]);
       dot2 = fma2(l[i], share[i], dot2);
     }
-    const float z = group_sum(z2.x + z2.y, tpr), dot = group_sum(dot2.x + dot2.y, tpr);
+    const float2 row_sums = group_sums(make_float2(z2.x + z2.y, dot2.x + dot2.y), tpr);
+    const float z = row_sums.x, dot = row_sums.y;
     const bool empty = z == 0.0f;
     const float inv_z = empty ? 0.0f : __fdividef(1.0f, z);  // z in [1, E]
     const float s = dot * inv_z;
@@ -375,34 +390,40 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const float2* __
 
 // After the counting kernel the losses may start early (they wait for its
 // result); without it they follow the caller's work as any launch does.
-template <int kValues, bool kVec, bool kFull>
+template <int kValues, bool kVec, bool kFull, int kTpr>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
+  constexpr auto kernel = loss_kernel<kValues, kVec, kFull, kTpr>;
   constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
-  const cudaError_t err = allow(reinterpret_cast<const void*>(loss_kernel<kValues, kVec, kFull>), done, 2 * operand, true);
+  const cudaError_t err = allow(reinterpret_cast<const void*>(kernel), done, 2 * operand, true);
   if (err != cudaSuccess) return err;
   const size_t smem = (args.a.d_in ? 2 : 1) * operand;
-  if (args.cluster) return launch_cluster(loss_kernel<kValues, kVec, kFull>, args.cluster, kThreads, smem, stream, args);
-  if (args.kept) return launch_dependent(loss_kernel<kValues, kVec, kFull>, grid, kThreads, smem, stream, args);
-  loss_kernel<kValues, kVec, kFull><<<grid, kThreads, smem, stream>>>(args);
+  if (args.cluster) return launch_cluster(kernel, args.cluster, kThreads, smem, stream, args);
+  if (args.kept) return launch_dependent(kernel, grid, kThreads, smem, stream, args);
+  kernel<<<grid, kThreads, smem, stream>>>(args);
   return cudaGetLastError();
 }
 
-template <bool kVec, bool kFull>
+template <bool kVec, bool kFull, int kTpr>
 cudaError_t launch_losses(const Args& args, int values, int grid, cudaStream_t stream) {
-  if (values <= 4) return launch_one<4, kVec, kFull>(args, grid, stream);
-  if (values <= 8) return launch_one<8, kVec, kFull>(args, grid, stream);
-  if (values <= 12) return launch_one<12, kVec, kFull>(args, grid, stream);
-  if (values <= 16) return launch_one<16, kVec, kFull>(args, grid, stream);
-  return launch_one<32, kVec, kFull>(args, grid, stream);
+  if constexpr (kTpr != 32) {  // rows of a whole warp have more
+    if (values <= 4) return launch_one<4, kVec, kFull, kTpr>(args, grid, stream);
+  }
+  if (values <= 8) return launch_one<8, kVec, kFull, kTpr>(args, grid, stream);
+  if (values <= 12) return launch_one<12, kVec, kFull, kTpr>(args, grid, stream);
+  if (values <= 16) return launch_one<16, kVec, kFull, kTpr>(args, grid, stream);
+  return launch_one<32, kVec, kFull, kTpr>(args, grid, stream);
 }
 
-// A row fills all of its lanes' values where E is so many: nothing to check.
+// A row fills all of its lanes' values where E is so many: nothing to check;
+// and a row of a whole warp then has its sizes known when compiling (65,536 x
+// 384: 60.5 us without, 58.3 with).
 cudaError_t launch_losses(const Args& args, bool vec, int values, int grid, cudaStream_t stream) {
-  if (!vec) return launch_losses<false, false>(args, values, grid, stream);
+  if (!vec) return launch_losses<false, false, 0>(args, values, grid, stream);
   const bool full = args.a.E == args.tpr * values && (values <= 16 || values == 32);
-  return full ? launch_losses<true, true>(args, values, grid, stream)
-              : launch_losses<true, false>(args, values, grid, stream);
+  if (!full) return launch_losses<true, false, 0>(args, values, grid, stream);
+  return args.tpr == 32 ? launch_losses<true, true, 32>(args, values, grid, stream)
+                        : launch_losses<true, true, 0>(args, values, grid, stream);
 }
 
 constexpr size_t kPartialBytes = kRouterLossMaxPieces * sizeof(float2);
