@@ -29,8 +29,8 @@
 //
 // Bound by instructions and their latency together: about 36 instructions a
 // value at half the SMs' issue slots, 55 % of the memory's rate (65,536 x 384
-// added to a gradient: 58 us with the last sums and 60 with a mask, of which
-// reading and writing alone are 45).
+// added to a gradient: 56.5 us with the last sums and 57.7 with a mask, of
+// which reading and writing alone are 45).
 #include "common.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -166,17 +166,22 @@ __device__ __forceinline__ float exp2_approx(float v) {
   return r;
 }
 
-// Rows in flight a group: this one and the next two, or the next one where a
-// lane has more than 16 values.
-template <int kValues>
-constexpr int kStages = kValues <= 16 ? 3 : 2;
-constexpr int kStealRounds = 8;  // at least the rows in flight
+// Rows in flight a group: this one and the next.  Blocks an SM: the registers
+// of a lane's values, and no more, bound them (65,536 x 384, 12 values a lane:
+// 5 blocks 56.6 us, 6 blocks 57.8, 7 blocks 60.7; 30,000 x 1,000, 32 values: 3
+// blocks 75.3 us, 4 blocks 84.5).
+constexpr int kStages = 2;
+constexpr int blocks_per_sm(int values) { return values <= 12 ? 5 : values <= 16 ? 4 : 3; }
+// Rounds of a stolen piece: no fewer than the rows in flight, so that only one
+// piece is ahead; few, so that the SMs end together (30,000 x 1,000: 8 rounds
+// 98.6 us, 4 rounds 87.1).
+constexpr int kStealRounds = 4;
 
 // kTpr: the lanes of a row where that is known when compiling, or 0.
 template <int kValues, bool kVec, bool kFull, int kTpr>
-__global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(const Args args) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(kValues)) loss_kernel(const Args args) {
   const RouterLoss& a = args.a;
-  constexpr int kPairsRow = kValues / 2, S = kStages<kValues>, kWarps = kThreads / 32;
+  constexpr int kPairsRow = kValues / 2, S = kStages, kWarps = kThreads / 32;
   constexpr uint32_t kOperand = kValues / (kVec ? 4 : 1) * kPitch<kVec>;
   const int tpr = kTpr ? kTpr : args.tpr, E = kFull && kTpr ? kValues * kTpr : a.E;
   extern __shared__ uint4 ring[];  // [stage][operand][vector or value][thread]
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kValues <= 12 ? 6 : 4) loss_kernel(c
         const float2 lo = l[i / 2];
         if (kVec) {
           const float2 hi = l[i / 2 + (kVec ? 1 : 0)];
-          if (kFull || e < E) *reinterpret_cast<float4*>(out + e) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          if (kFull || e < E) __stcs(reinterpret_cast<float4*>(out + e), make_float4(lo.x, lo.y, hi.x, hi.y));
         } else {
           if (e < E) out[e] = lo.x;
           if (e + tpr < E) out[e + tpr] = lo.y;
@@ -394,7 +399,7 @@ template <int kValues, bool kVec, bool kFull, int kTpr>
 cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr auto kernel = loss_kernel<kValues, kVec, kFull, kTpr>;
-  constexpr size_t operand = kStages<kValues> * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
+  constexpr size_t operand = kStages * (kValues / (kVec ? 4 : 1)) * static_cast<size_t>(kPitch<kVec>);
   const cudaError_t err = allow(reinterpret_cast<const void*>(kernel), done, 2 * operand, true);
   if (err != cudaSuccess) return err;
   const size_t smem = (args.a.d_in ? 2 : 1) * operand;
@@ -456,7 +461,7 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
     args.rounds = static_cast<int>((want + args.cluster - 1) / args.cluster);
     return launch_losses(args, vec, values, 0, stream);
   }
-  const int64_t resident = num_sms * (values <= 12 ? 6 : 4);
+  const int64_t resident = num_sms * blocks_per_sm(values);
   int64_t rounds = (want + resident - 1) / resident;
   if (rounds >= 2 * kStealRounds) {
     args.steal = true;
