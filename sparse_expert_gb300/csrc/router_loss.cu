@@ -409,15 +409,22 @@ cudaError_t launch_one(const Args& args, int grid, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Only the combinations that the choice of lanes leads to: vectors with lanes
+// of fewer than 8 values are a row of 4 in one lane; a full row of less than a
+// warp has at most 12 values a lane.
 template <bool kVec, bool kFull, int kTpr>
 cudaError_t launch_losses(const Args& args, int values, int grid, cudaStream_t stream) {
-  if constexpr (kTpr != 32) {  // rows of a whole warp have more
+  constexpr bool kFullFew = kFull && kTpr == 0;
+  if constexpr (!kVec || kFullFew) {
     if (values <= 4) return launch_one<4, kVec, kFull, kTpr>(args, grid, stream);
   }
   if (values <= 8) return launch_one<8, kVec, kFull, kTpr>(args, grid, stream);
-  if (values <= 12) return launch_one<12, kVec, kFull, kTpr>(args, grid, stream);
-  if (values <= 16) return launch_one<16, kVec, kFull, kTpr>(args, grid, stream);
-  return launch_one<32, kVec, kFull, kTpr>(args, grid, stream);
+  if (kFullFew || values <= 12) return launch_one<12, kVec, kFull, kTpr>(args, grid, stream);
+  if constexpr (!kFullFew) {
+    if (values <= 16) return launch_one<16, kVec, kFull, kTpr>(args, grid, stream);
+    return launch_one<32, kVec, kFull, kTpr>(args, grid, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // A row fills all of its lanes' values where E is so many: nothing to check;
@@ -445,8 +452,8 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
   const bool vec = a.E % 4 == 0 && low % 16 == 0;
   // few lanes with up to 12 values each (16 single ones): a row's reductions
   // cost as much as a dozen values of every lane that takes part (60,000 x 64
-  // with 4, 12 and 16 values a lane: 16.6, 13.9 and 16.1 us; 65,536 x 384 with
-  // 12 and 24: 60.7 and 63.3 us)
+  // with 12 and 16 values a lane: 13.3 and 15.5 us; 65,536 x 384 with 12 and 24:
+  // 56.2 and 59.8 us)
   const int units = vec ? a.E / 4 : a.E, per = vec ? 3 : 16;
   while (args.tpr < 32 && args.tpr * per < units) args.tpr *= 2;
   const int values = (units + args.tpr - 1) / args.tpr * (vec ? 4 : 1);
