@@ -306,14 +306,16 @@ int grid_of(int64_t T, int groups, int most) {
   return static_cast<int>(want < most ? want : most);
 }
 
-// Blocks of a ring kernel with `groups` groups each, `resident` at a time.
-// With rows that do not start on a chunk, all blocks together take a multiple
-// of `values` rows a round (`values` is a power of two, and so is `groups`).
+// Blocks of a ring kernel with `groups` groups each, `resident` at a time:
+// never more than there are rows, which is what the backward's workspace holds
+// partial sums for.  A block for each of its groups' rows where they are few
+// enough: no group then has a second row.  Else, with rows that do not start
+// on a chunk, all blocks together take a multiple of `values` rows a round
+// (`values` is a power of two, and so is `groups`).
 int ring_grid(int64_t T, int groups, int values, bool aligned, int resident) {
-  const int multiple = aligned || groups >= values ? 1 : values / groups;
   const int grid = grid_of(T, groups, resident);
-  const int up = (grid + multiple - 1) / multiple * multiple;
-  return up <= resident ? up : resident / multiple * multiple;
+  const int multiple = aligned || groups >= values ? 1 : values / groups;
+  return grid < resident ? grid : resident / multiple * multiple;
 }
 
 // How rows lie: on chunks, or all alike within 16 bytes, or neither.  Each

@@ -209,6 +209,23 @@ def test_backward_strides_and_alignment(moe, d, stride, shift, dtype):
     backward_case(moe, 40, d, dtype, torch.float32, residual=True, seed=d, stride=stride, shift=shift)
 
 
+@pytest.mark.parametrize("T,d,dtype,offset", [
+    (T, 6145, dtype, 0) for dtype in (torch.bfloat16, torch.float16) for T in (33, 41, 151)
+] + [(33, 3073, torch.float32, 0), (151, 3073, torch.float32, 0), (77, 6144, torch.bfloat16, 1), (60, 16001, torch.float16, 0),
+     (93, 2049, torch.bfloat16, 0), (93, 20001, torch.bfloat16, 0), (93, 1001, torch.float32, 1)])
+def test_backward_stays_in_its_workspace(moe, T, d, dtype, offset):
+    """Rows off a chunk (or, with an offset, weights off 16 bytes), no multiple
+    of a chunk's values of them: what lies behind the workspace is not touched."""
+    z, dy = rows(T, d, dtype, seed=T, offset=0.5), rows(T, d, dtype, seed=T + 1, scale=0.1)
+    w = params(d + offset, torch.float32, seed=3)[0][offset:]
+    stats = torch.stack(exact_stats(z)).float()
+    size = moe.moe_layer_norm_backward_workspace_bytes(T, d)
+    buf = torch.full((size + (4 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = moe.moe_layer_norm_backward(dy, z, stats, w, workspace=buf[:size])
+    check_backward(dy, z, stats, w, None, got)
+    assert torch.all(buf[size:] == 0xA5)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("d", [192, 30000])
 def test_backward_optional_outputs(moe, weight, bias, d):
