@@ -102,6 +102,29 @@ def test_forward_strides_and_alignment(moe, d, stride, shift, dtype):
     check_forward(z, w, b, y, stats)
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("T,d,dtype", [
+    (110003, 128, torch.bfloat16), (120011, 136, torch.float16),           # one chunk a thread
+    (20003, 1024, torch.bfloat16), (9001, 2048, torch.bfloat16), (5003, 2048, torch.float32),
+    (5001, 2056, torch.float16), (2503, 6144, torch.bfloat16), (1203, 16384, torch.bfloat16)])
+def test_forward_many_rows(moe, T, d, dtype, residual):
+    """More pieces than the SMs hold at once, so that blocks go on from piece
+    to piece, the last of them partial: every row right, and the same bits
+    whichever block takes it."""
+    x = rows(T, d, dtype, seed=T)
+    r = rows(T, d, dtype, seed=T + 1, scale=0.5) if residual else None
+    w, b = params(d, torch.float32, seed=5)
+    first = moe.moe_layer_norm(x, w, b, residual=r)
+    z = x
+    if residual:
+        z = first[2]
+        assert torch.equal(z, (x.float() + r.float()).to(dtype))
+    check_forward(z, w, b, *first[:2])
+    for _ in range(3):
+        again = moe.moe_layer_norm(x, w, b, residual=r)
+        assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
 @pytest.mark.parametrize("w,b", [(False, False), (True, False), (False, True)])
 def test_forward_without_weight_or_bias(moe, w, b):
     x = rows(50, 320, torch.bfloat16, seed=3)

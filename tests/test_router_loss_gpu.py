@@ -87,6 +87,21 @@ def test_many_rows(moe, T, E):
     check(moe, logits, counts, mask, d_in=torch.randn(T, E, device="cuda") * 1e-5)
 
 
+@pytest.mark.parametrize("T,E", [(22003, 384), (90001, 64), (13003, 768), (13001, 1000), (13007, 1023)])
+def test_more_pieces_than_blocks(moe, T, E):
+    """Blocks go on from piece to piece, the last of them partial: every row
+    right, and the same bits whichever block takes it."""
+    logits, counts, mask = inputs(T, E, seed=T)
+    d_in = torch.randn(T, E, device="cuda") * 1e-5
+    check(moe, logits, counts, None)
+    check(moe, logits, counts, None, d_in=d_in)
+    check(moe, logits, counts, mask)
+    first = check(moe, logits, counts, mask, d_in=d_in)
+    for _ in range(3):
+        again = moe.moe_router_loss(logits, counts, 0.02, 0.003, mask=mask, accumulate=d_in.clone())
+        assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
 def test_unaligned_rows(moe):
     buf = torch.randn(200 * 64 + 1, device="cuda")
     logits = buf[1:].view(200, 64)
