@@ -592,7 +592,11 @@ MOE_API moe_status_t moe_forward_host_stream(const void* const* x_host, const fl
  * The training step around the layer: the norm before it, the auxiliary
  * losses of its router, the norm of its gradients and the AdamW step over
  * them.  None of the four waits for the GPU or needs a status word; each
- * gives the same bits for the same inputs on every call.
+ * gives the same bits for the same inputs on every call.  The layer norm and
+ * the router losses have one wait, for the GPU's own answer about the next
+ * piece of work, which ends after 4 s: should the answer never come, rows may
+ * be left unwritten, and NaN stands in the statistics and y of a row, or in
+ * both losses.
  * ---------------------------------------------------------------------- */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype_t;
 
@@ -766,6 +770,16 @@ MOE_API moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_
  * ---------------------------------------------------------------------- */
 MOE_API moe_status_t moe_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int64_t limit_ns,
                                        moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Check of the block-wide wait of the kernels that take further pieces of
+ * work (layer norm, router losses): all threads of a block come to the same
+ * outcome.  out [256] int32 on the device: for each of 128 threads 0, from a
+ * wait for something that never comes (limit_ns: 1 .. 2e9 ns), then 1, from
+ * one that comes after all threads but one have run out of time.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+MOE_API moe_status_t moe_selftest_steal_wait(int32_t* out, int64_t limit_ns, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Reads the device status word at the start of a workspace used by

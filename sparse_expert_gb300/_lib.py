@@ -99,6 +99,7 @@ SIGNATURES = {
     "moe_get_device_status": (_S, [_P, _P]),
     "moe_dispatch_noalloc_status": (_S, [_P, ctypes.POINTER(_I32)]),
     "moe_selftest_wait_timeout": (_S, [_P, _SZ, _I64, _P]),
+    "moe_selftest_steal_wait": (_S, [_P, _I64, _P]),
     "moe_selftest_activation": (_S, [_P, _I64, _P, _P, _P]),
     "moe_set_tile_schedule": (_S, [_I32]),
     "moe_occupy_sms": (_S, [_I32, _I64, _P]),
@@ -619,6 +620,13 @@ def moe_selftest_wait_timeout(workspace, limit_ns, stream=None):
     """Runs the bounded-wait check; read the status with moe_read_device_status."""
     _check(lib.moe_selftest_wait_timeout(_ptr(workspace), workspace.numel(), int(limit_ns), _stream(stream)),
            "moe_selftest_wait_timeout")
+
+
+def moe_selftest_steal_wait(limit_ns, stream=None):
+    """Outcomes [2, 128] of the block-wide wait: nothing comes, and it comes late."""
+    out = torch.empty(2, 128, dtype=torch.int32, device="cuda")
+    _check(lib.moe_selftest_steal_wait(_ptr(out), int(limit_ns), _stream(stream)), "moe_selftest_steal_wait")
+    return out
 
 
 def moe_selftest_activation(z, stream=None):

@@ -1008,6 +1008,18 @@ moe_status_t moe_backward_timed(const void* x, const float* logits, const void* 
                        workspace, workspace_bytes, stream, events);
 }
 
+moe_status_t moe_selftest_steal_wait(int32_t* out, int64_t limit_ns, moe_stream_t stream) {
+  if (limit_ns < 1 || limit_ns > static_cast<int64_t>(kWaitLimitNs))
+    return fail(MOE_ERR_INVALID_ARG, "limit_ns must be in [1, 2e9]");
+  if (!out || !aligned(out, 4)) return fail(MOE_ERR_INVALID_ARG, "out is NULL or misaligned");
+  DeviceInfo dev;
+  moe_status_t s = device_info(&dev);
+  if (s != MOE_OK) return s;
+  MOE_CUDA(launch_steal_wait(out, static_cast<uint64_t>(limit_ns), static_cast<cudaStream_t>(stream)),
+           "steal wait check launch");
+  return MOE_OK;
+}
+
 moe_status_t moe_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int64_t limit_ns,
                                        moe_stream_t stream) {
   if (limit_ns < 1 || limit_ns > static_cast<int64_t>(kWaitLimitNs))

@@ -300,6 +300,9 @@ cudaError_t launch_adamw(const moe_adamw_tensor_t* tensors, int n_tensors, const
 // Bounded-wait check: one block waits on a phase that never completes and
 // records a timeout in *status after limit_ns.
 cudaError_t launch_wait_timeout(int32_t* status, uint64_t limit_ns, cudaStream_t stream);
+
+// Check of the block-wide wait for stolen work; out: 256 outcomes.
+cudaError_t launch_steal_wait(int32_t* out, uint64_t limit_ns, cudaStream_t stream);
 cudaError_t launch_activation(const float* z, int64_t n, float* silu, float* sigmoid, int num_sms,
                               cudaStream_t stream);
 

@@ -27,6 +27,8 @@ namespace moe {
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+constexpr int kStealRefused = -1, kStealUnanswered = -2;
+
 // Asks for a launch to cancel; the answer (16 bytes, in `answer`) completes the
 // barrier's phase.  One thread; not again after a refusal.
 __device__ __forceinline__ void steal_request(uint4* answer, uint64_t* bar) {
@@ -36,7 +38,7 @@ __device__ __forceinline__ void steal_request(uint4* answer, uint64_t* bar) {
                "r"(smem_addr(bar))
                : "memory");
 }
-// The x index of the block whose launch was cancelled, or -1.
+// The x index of the block whose launch was cancelled, or kStealRefused.
 __device__ __forceinline__ int steal_answer(const uint4* answer) {
   uint32_t x = 0, ok;
   asm volatile(
@@ -49,8 +51,45 @@ __device__ __forceinline__ int steal_answer(const uint4* answer) {
       : "=r"(x), "=r"(ok)
       : "r"(smem_addr(answer))
       : "memory");
-  return ok ? static_cast<int>(x) : -1;
+  return ok ? static_cast<int>(x) : kStealRefused;
 }
+
+// Waits for an answer, for limit_ns at most; looks once more after that, for a
+// block that was off its SM meanwhile.
+__device__ __forceinline__ bool steal_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint32_t a = smem_addr(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  do {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(a, parity)) return true;
+  } while (global_timer_ns() - t0 <= limit_ns);
+  return mbar_try_wait(a, parity);
+}
+
+// All threads of the block, each with its own limit: true in every one of them
+// where the answer came to any, so that they go on alike.
+__device__ __forceinline__ bool steal_told(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return __syncthreads_or(steal_wait(bar, parity, limit_ns));
+}
+
+// All threads of the block: the index of the block whose launch was cancelled,
+// kStealRefused, or kStealUnanswered after twice the limit.  A launch that was
+// cancelled starts nowhere else, so an answer that some threads have not seen
+// in time is waited for again and taken by all, and one that never came may
+// have been a piece of work: the caller must let that be seen.
+__device__ __forceinline__ int steal_next(const uint4* answer, uint64_t* bar, uint32_t parity) {
+  const bool told = steal_wait(bar, parity, kWaitLimitNs);
+  int block = told ? steal_answer(answer) : kStealRefused;
+  if (__syncthreads_and(block >= 0)) return block;  // and all have read it
+  if (!steal_told(bar, parity, kWaitLimitNs)) return kStealUnanswered;
+  block = steal_answer(answer);
+  __syncthreads();
+  return block;
+}
+
+// What a kernel keeps of its requests: the number of answers so far, or one of
+constexpr uint32_t kStealOver = ~0u, kStealLost = ~0u - 1;  // refused; unanswered
 
 constexpr int kClusterMost = 16;  // above 8 needs the kernel's leave (allow_cluster)
 

@@ -41,7 +41,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
   __shared__ float2 red[2][B * kMaxWarps];
   __shared__ uint4 answer;
   __shared__ uint64_t answer_bar;
-  __shared__ volatile int give_up;  // the bounded wait's other way out, unused
   constexpr bool kOneGroup = kTpr >= kOwnBlock;  // the block is the group
   const int groups = kOneGroup ? 1 : (kTpr ? kSmallBlock : blockDim.x) / tpr;
   const int lane = kOneGroup ? threadIdx.x : threadIdx.x % tpr, group = kOneGroup ? 0 : threadIdx.x / tpr;
@@ -54,7 +53,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
   const int64_t first = blockIdx.x * a.piece + group;
   const int64_t end = kAligned && !a.steal ? min(a.T, (blockIdx.x + 1) * a.piece) : a.T;
   if (kAligned && a.steal && threadIdx.x == 0) {
-    give_up = 0;
     mbar_init(&answer_bar, 1);
     fence_barrier_init();
     steal_request(&answer, &answer_bar);
@@ -90,15 +88,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
     if (!kAligned || ++ahead_round < a.tile_rounds) return;
     ahead_round = 0;
     next_piece = ahead = a.T;
-    if (!a.steal || answers == ~0u) return;
+    if (!a.steal || answers >= kStealLost) return;
     if (answers == 0) __syncthreads();  // the barrier is initialised
-    const bool told = mbar_wait(&answer_bar, answers & 1, &give_up);
-    const int block = told ? steal_answer(&answer) : -1;
-    // an answer that did not come in time is taken as a refusal: launches
-    // that were not cancelled start as blocks of their own
-    const bool stolen = __syncthreads_and(block >= 0);  // and all have read it
-    answers = stolen ? answers + 1 : ~0u;
-    if (!stolen) return;
+    const int block = steal_next(&answer, &answer_bar, answers & 1);
+    answers = block >= 0 ? answers + 1 : block == kStealRefused ? kStealOver : kStealLost;
+    if (block < 0) return;
     if (threadIdx.x == 0) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       steal_request(&answer, &answer_bar);
@@ -232,7 +226,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const For
     y += B * out_step;
     if (res) z += B * out_step;
     if (++round < a.tile_rounds) continue;
-    if (next_piece >= a.T) return;
+    if (next_piece >= a.T) {
+      // a piece may be lost: NaN in the first row of this one (which this
+      // thread wrote) says so
+      if (answers == kStealLost && threadIdx.x == 0) {
+        const int64_t row = t - a.piece;
+        a.stats[row] = a.stats[a.T + row] = nanf("");
+        static_cast<T*>(a.y)[row * a.d] = from_f32<T>(nanf(""));
+      }
+      return;
+    }
     round = 0;
     t = next_piece + group;
     y = static_cast<T*>(a.y) + t * a.d;

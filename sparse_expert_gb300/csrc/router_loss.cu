@@ -189,11 +189,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kValues)) loss_kernel(
   __shared__ float2 red[2][kWarps], block_losses;
   __shared__ uint4 answer;
   __shared__ uint64_t answer_bar;
-  __shared__ volatile int give_up;  // the bounded wait's other way out, unused
   let_next_start();
   const int lane = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = kThreads / tpr;
   if (args.steal && threadIdx.x == 0) {
-    give_up = 0;
     mbar_init(&answer_bar, 1);
     fence_barrier_init();
     steal_request(&answer, &answer_bar);
@@ -223,15 +221,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kValues)) loss_kernel(
       ahead_round = 0;
       next_piece = -1;
       ahead = a.T;
-      if (args.steal && answers != ~0u) {
+      if (args.steal && answers < kStealLost) {
         if (answers == 0) __syncthreads();  // the barrier is initialised
-        const bool told = mbar_wait(&answer_bar, answers & 1, &give_up);
-        const int block = told ? steal_answer(&answer) : -1;
-        // an answer that did not come in time is taken as a refusal:
-        // launches that were not cancelled start as blocks of their own
-        const bool stolen = __syncthreads_and(block >= 0);  // and all have read it
-        answers = stolen ? answers + 1 : ~0u;
-        if (stolen) {
+        const int block = steal_next(&answer, &answer_bar, answers & 1);
+        answers = block >= 0 ? answers + 1 : block == kStealRefused ? kStealOver : kStealLost;
+        if (block >= 0) {
           if (threadIdx.x == 0) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             steal_request(&answer, &answer_bar);
@@ -345,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(kValues)) loss_kernel(
       sums = red[parity][0];
 #pragma unroll
       for (int i = 1; i < kWarps; ++i) sums = add2(sums, red[parity][i]);
+      if (answers == kStealLost) sums = both(nanf(""));  // a piece may be lost: both losses say so
       if (args.cluster) block_losses = sums;
       else args.partial[piece] = sums;
     }
