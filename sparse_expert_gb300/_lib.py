@@ -964,7 +964,8 @@ def moe_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, masters=No
     n_tensors = len(params)
     m_scales, v_scales, masters = (([None] * n_tensors) if a is None else a for a in (m_scales, v_scales, masters))
     decay = [1.0] * n_tensors if decay is None else decay
-    every = (params, grads, m, v, m_scales, v_scales, masters, decay)
+    # copies of the lists: the plan keeps the tensors, whatever the caller does with the lists
+    every = tuple(tuple(a) for a in (params, grads, m, v, m_scales, v_scales, masters, decay))
     if any(len(a) != n_tensors for a in every):
         raise ValueError("the lists must have one entry for each parameter")
     buf = bytearray(_RECORD.size * n_tensors)

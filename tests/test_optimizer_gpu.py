@@ -5,7 +5,9 @@ and sums are rounded one by one.
 Tolerances: u = 2^-24 for each fp32 operation and each coefficient; m and v
 take at most five each, the update at most twelve more.
 """
+import gc
 import math
+import weakref
 
 import pytest
 import torch
@@ -184,6 +186,20 @@ def test_lists_of_any_length(moe, n_tensors):
     out = moe.moe_grad_norm(plan, max_norm=want / 2 if want else 1.0)
     assert abs(out[0].item() - want) <= 400 * U * want
     assert abs(out[1].item() - (0.5 if want else 1.0)) <= 400 * U
+
+
+def test_plans_keep_their_tensors(moe):
+    """Emptying the lists that a plan was made from frees nothing that its records point to."""
+    lists = tensors([1000, 77], torch.bfloat16, torch.bfloat16, True, 8, seed=6)
+    plan = plan_of(moe, lists)
+    grads = [torch.ones(50, device="cuda") for _ in range(3)]
+    listed = moe.moe_tensor_list(grads)
+    kept = [weakref.ref(t) for ts in (*lists.values(), grads) for t in ts]
+    for ts in (*lists.values(), grads):
+        ts.clear()
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    assert len(plan) == 2 and len(listed) == 3
 
 
 def test_neighbours_are_not_touched(moe):
