@@ -707,12 +707,46 @@ def moe_dispatch_noalloc_status(stream=None) -> int:
 # while the other stream's kernel still uses it.
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # moe_dtype_t
 _raw_stream = torch._C._cuda_getCurrentRawStream  # cudaStream_t of the current stream of a device index
+_current_device = torch._C._cuda_getDevice
 
 
-def _rows(t, name, shape=None, dtype=None):
-    """Checks a [T, d] tensor of rows (unit stride along d) and returns its row stride."""
+def _elsewhere(t, name, index):
+    """Raises for a tensor that is not on device `index`."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _here(index, name):
+    """Raises unless device `index` is the one that the call launches on: the
+    current device, or that of the call's stream."""
+    if index != _current_device():
+        raise ValueError(f"{name} must be on the current device (or the stream's), cuda:{_current_device()}, "
+                         f"got cuda:{index}")
+
+
+def _device_of(t, name):
+    """Index of the device of a call's first operand, which the others share."""
+    index = t.get_device()
+    if index < 0:
+        _elsewhere(t, name, index)
+    _here(index, name)
+    return index
+
+
+def _workspace(t, index):
+    """Bytes of a caller's workspace."""
+    if t.get_device() != index:
+        _elsewhere(t, "workspace", index)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
+def _rows(t, name, index, shape=None, dtype=None):
+    """Checks a [T, d] tensor of rows (unit stride along d) and returns its row stride."""
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
     if t.dtype is not dtype and (dtype is not None or t.dtype not in _DTYPES):
         raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
     if t.dim() != 2 or (shape is not None and t.shape != shape):
@@ -723,20 +757,24 @@ def _rows(t, name, shape=None, dtype=None):
     return stride[0]
 
 
-def _norm_param(t, name, d, dtype):
+def _norm_param(t, name, index, d, dtype):
     """Checks a weight or bias [d] and returns its moe_dtype_t."""
     wdt = t.dtype
     if wdt is not dtype and wdt is not torch.float32:
         raise TypeError(f"{name} must be float32 or {dtype}, got {wdt}")
     if t.shape != (d,):
         raise ValueError(f"{name} must be [{d}], got {list(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    if not t.is_contiguous():
         _contig(t, wdt, name)
     return _DTYPES[wdt]
 
 
-def _out(t, shape, dtype, name):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+def _out(t, index, shape, dtype, name):
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    if t.dtype is not dtype or not t.is_contiguous():
         _contig(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -750,34 +788,35 @@ def moe_layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None,
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_layer_norm(x, weight, bias, eps, residual, out, stats, z)
-    x_stride = _rows(x, "x")
+    index = _device_of(x, "x")
+    x_stride = _rows(x, "x", index)
     shape, dt = x.shape, x.dtype
     T, d = shape
     code = wcode = _DTYPES[dt]
     w_ptr = b_ptr = r_ptr = z_ptr = None
     r_stride = 0
     if weight is not None:
-        wcode = _norm_param(weight, "weight", d, dt)
+        wcode = _norm_param(weight, "weight", index, d, dt)
         w_ptr = weight.data_ptr()
     if bias is not None:
-        bcode = _norm_param(bias, "bias", d, dt)
+        bcode = _norm_param(bias, "bias", index, d, dt)
         if weight is not None and bcode != wcode:
             raise TypeError("weight and bias must have one type")
         wcode, b_ptr = bcode, bias.data_ptr()
     dev = x.device
     if residual is not None:
-        r_stride, r_ptr = _rows(residual, "residual", shape, dt), residual.data_ptr()
-        z = torch.empty(shape, dtype=dt, device=dev) if z is None else _out(z, shape, dt, "z")
+        r_stride, r_ptr = _rows(residual, "residual", index, shape, dt), residual.data_ptr()
+        z = torch.empty(shape, dtype=dt, device=dev) if z is None else _out(z, index, shape, dt, "z")
         z_ptr = z.data_ptr()
     elif z is not None:
         raise ValueError("z is written with a residual only")
-    out = torch.empty(shape, dtype=dt, device=dev) if out is None else _out(out, shape, dt, "out")
+    out = torch.empty(shape, dtype=dt, device=dev) if out is None else _out(out, index, shape, dt, "out")
     if stats is None:
         stats = torch.empty((2, T), dtype=torch.float32, device=dev)
     else:
-        _out(stats, (2, T), torch.float32, "stats")
+        _out(stats, index, (2, T), torch.float32, "stats")
     status = lib.moe_layer_norm(x.data_ptr(), x_stride, r_ptr, r_stride, w_ptr, b_ptr, T, d, code, wcode, eps,
-                                out.data_ptr(), z_ptr, stats.data_ptr(), _raw_stream(dev.index))
+                                out.data_ptr(), z_ptr, stats.data_ptr(), _raw_stream(index))
     if status:
         _check(status, "moe_layer_norm")
     return (out, stats) if residual is None else (out, stats, z)
@@ -796,19 +835,20 @@ def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_layer_norm_backward(dy, z, stats, weight, bias, dz, grads, workspace)
-    dy_stride = _rows(dy, "dy")
+    index = _device_of(dy, "dy")
+    dy_stride = _rows(dy, "dy", index)
     shape, dt, dev = dy.shape, dy.dtype, dy.device
     T, d = shape
-    z_stride = _rows(z, "z", shape, dt)
+    z_stride = _rows(z, "z", index, shape, dt)
     code = wcode = _DTYPES[dt]
     w_ptr = dz_ptr = dw_ptr = db_ptr = None
     if weight is not None:
-        wcode = _norm_param(weight, "weight", d, dt)
+        wcode = _norm_param(weight, "weight", index, d, dt)
         w_ptr = weight.data_ptr()
-    _out(stats, (2, T), torch.float32, "stats")
+    _out(stats, index, (2, T), torch.float32, "stats")
     dz_stride = 0
     if dz is not None:
-        dz_stride, dz_ptr = _rows(dz, "dz", shape, dt), dz.data_ptr()
+        dz_stride, dz_ptr = _rows(dz, "dz", index, shape, dt), dz.data_ptr()
     if grads is None:
         grads = dict(dx=torch.empty(shape, dtype=dt, device=dev),
                      dweight=torch.empty(d, dtype=torch.float32, device=dev) if weight is not None else None,
@@ -816,11 +856,11 @@ def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads
         dw, db = grads["dweight"], grads["dbias"]
     else:
         dw, db = grads["dweight"], grads["dbias"]
-        _out(grads["dx"], shape, dt, "dx")
+        _out(grads["dx"], index, shape, dt, "dx")
         if dw is not None:
-            _out(dw, (d,), torch.float32, "dweight")
+            _out(dw, index, (d,), torch.float32, "dweight")
         if db is not None:
-            _out(db, (d,), torch.float32, "dbias")
+            _out(db, index, (d,), torch.float32, "dbias")
     if dw is not None:
         dw_ptr = dw.data_ptr()
     if db is not None:
@@ -829,10 +869,10 @@ def moe_layer_norm_backward(dy, z, stats, weight=None, bias=True, dz=None, grads
         size = moe_layer_norm_backward_workspace_bytes(T, d)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
-        size = workspace.numel()
+        size = _workspace(workspace, index)
     status = lib.moe_layer_norm_backward(dy.data_ptr(), dy_stride, z.data_ptr(), z_stride, stats.data_ptr(), w_ptr,
                                          dz_ptr, dz_stride, T, d, code, wcode, grads["dx"].data_ptr(), dw_ptr, db_ptr,
-                                         workspace.data_ptr(), size, _raw_stream(dev.index))
+                                         workspace.data_ptr(), size, _raw_stream(index))
     if status:
         _check(status, "moe_layer_norm_backward")
     return grads
@@ -853,35 +893,36 @@ def moe_router_loss(logits, counts, balance_coef=0.01, z_coef=0.001, mask=None, 
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_router_loss(logits, counts, balance_coef, z_coef, mask, accumulate, out, losses, workspace)
+    index = _device_of(logits, "logits")
     _contig(logits, torch.float32, "logits")
     shape, dev = logits.shape, logits.device
     T, E = shape
-    _out(counts, (E,), torch.int32, "counts")
+    _out(counts, index, (E,), torch.int32, "counts")
     m_ptr = a_ptr = None
     if mask is not None:
         if mask.dtype not in (torch.bool, torch.uint8):
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
-        m_ptr = _out(mask, (T,), mask.dtype, "mask").data_ptr()
+        m_ptr = _out(mask, index, (T,), mask.dtype, "mask").data_ptr()
     if accumulate is not None:
         if out is not None:
             raise ValueError("accumulate is written in place: give it or out")
-        out = _out(accumulate, shape, torch.float32, "accumulate")
+        out = _out(accumulate, index, shape, torch.float32, "accumulate")
         a_ptr = out.data_ptr()
     elif out is None:
         out = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
-        _out(out, shape, torch.float32, "out")
+        _out(out, index, shape, torch.float32, "out")
     if losses is None:
         losses = torch.empty(2, dtype=torch.float32, device=dev)
     else:
-        _out(losses, (2,), torch.float32, "losses")
+        _out(losses, index, (2,), torch.float32, "losses")
     if workspace is None:
         size = _ROUTER_LOSS_WORKSPACE
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
-        size = workspace.numel()
+        size = _workspace(workspace, index)
     status = lib.moe_router_loss(logits.data_ptr(), counts.data_ptr(), m_ptr, T, E, balance_coef, z_coef, a_ptr,
-                                 out.data_ptr(), losses.data_ptr(), workspace.data_ptr(), size, _raw_stream(dev.index))
+                                 out.data_ptr(), losses.data_ptr(), workspace.data_ptr(), size, _raw_stream(index))
     if status:
         _check(status, "moe_router_loss")
     return losses, out
@@ -1003,17 +1044,19 @@ def moe_grad_norm(tensors, max_norm=float("inf"), out=None, workspace=None, stre
     if not isinstance(tensors, TensorList):
         tensors = moe_tensor_list(tensors)
     dev = tensors.device
+    index = dev.index
+    _here(index, "tensors")
     if out is None:
         out = torch.empty(2, dtype=torch.float32, device=dev)
     else:
-        _out(out, (2,), torch.float32, "out")
+        _out(out, index, (2,), torch.float32, "out")
     if workspace is None:
         size = _GRAD_NORM_WORKSPACE
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
-        size = workspace.numel()
+        size = _workspace(workspace, index)
     status = lib.moe_grad_norm(tensors.address, tensors.count, max_norm, out.data_ptr(), workspace.data_ptr(), size,
-                               _raw_stream(dev.index))
+                               _raw_stream(index))
     if status:
         _check(status, "moe_grad_norm")
     return out
@@ -1036,13 +1079,18 @@ def moe_adamw_step(plan, lr=None, step=None, betas=(0.9, 0.95), eps=1e-8, weight
     weight_decay."""
     if not plan.has_states:
         raise ValueError("moe_adamw_step needs a plan from moe_adamw_plan")
+    index = plan.device.index
+    if stream is not None and index != _current_device():
+        with torch.cuda.stream(stream):
+            return moe_adamw_step(plan, lr, step, betas, eps, weight_decay, clip, hyper)
+    _here(index if stream is None else stream.device.index, "plan")
     scale = None
     if clip is not None:
-        scale = _out(clip, (2,), torch.float32, "clip").data_ptr() + 4
+        scale = _out(clip, index, (2,), torch.float32, "clip").data_ptr() + 4
     if hyper is not None:
         if lr is not None or step is not None:
             raise ValueError("give hyper, or lr and step")
-        host, dev = None, _out(hyper, (8,), torch.float32, "hyper").data_ptr()
+        host, dev = None, _out(hyper, index, (8,), torch.float32, "hyper").data_ptr()
     else:
         if lr is None or step is None:
             raise ValueError("lr and step are needed without hyper")
@@ -1052,6 +1100,6 @@ def moe_adamw_step(plan, lr=None, step=None, betas=(0.9, 0.95), eps=1e-8, weight
         if status:
             _check(status, "moe_adamw_hyper")
     status = lib.moe_adamw_step(plan.address, plan.count, host, dev, scale,
-                                _raw_stream(plan.device.index) if stream is None else stream.cuda_stream)
+                                _raw_stream(index) if stream is None else stream.cuda_stream)
     if status:
         _check(status, "moe_adamw_step")
