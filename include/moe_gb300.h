@@ -712,7 +712,7 @@ MOE_API moe_status_t moe_router_loss(const float* logits, const int32_t* counts,
  *               not finite the call changes nothing (the step is skipped).
  * Tensors with n = 0 are skipped.  Tensors must not overlap.  A tensor whose
  * pointers are 32-byte aligned runs fastest; the scales need 4-byte
- * alignment, the rest that of their type.
+ * alignment, the rest that of their type.  Supported: n <= 2^42 - 2048.
  *
  * moe_adamw_hyper: the record for one step (host only, computed in fp64).
  * Needs lr, weight_decay, eps >= 0, 0 <= beta < 1, step >= 1, all finite.
@@ -724,8 +724,8 @@ MOE_API moe_status_t moe_router_loss(const float* logits, const int32_t* counts,
  *            infinite).  max_norm = infinity: never clipped.
  *   Squares are summed in fp32 by each thread and in fp64 over threads, in a
  *   fixed order.  Workspace: moe_grad_norm_workspace_bytes() bytes.
- * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE, MOE_ERR_NO_DEVICE,
- *         MOE_ERR_CUDA.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 typedef struct {
   void* param;

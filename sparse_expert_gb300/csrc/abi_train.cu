@@ -67,7 +67,7 @@ moe_status_t check_list(const moe_adamw_tensor_t* tensors, int32_t n_tensors, bo
   for (int32_t i = 0; i < n_tensors; ++i) {
     const moe_adamw_tensor_t& t = tensors[i];
     if (t.n < 0) return fail(MOE_ERR_INVALID_ARG, "a tensor's n must not be negative");
-    if (t.n >= (int64_t(1) << 42)) return fail(MOE_ERR_UNSUPPORTED, "a tensor's n must be below 2^42");
+    if (t.n > kTensorMaxValues) return fail(MOE_ERR_UNSUPPORTED, "a tensor's n must be at most 2^42 - 2048");
     if (!known(t.grad_type)) return fail(MOE_ERR_UNSUPPORTED, "grad_type must be MOE_F32, MOE_BF16 or MOE_F16");
     if (t.n == 0) continue;
     if (!t.grad) return fail(MOE_ERR_INVALID_ARG, "NULL gradient");

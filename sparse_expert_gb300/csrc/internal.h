@@ -291,6 +291,8 @@ cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t st
 
 // The optimizer's lists of tensors (arrays in host memory).
 constexpr int kGradNormMaxBlocks = 4096;
+constexpr int kAdamWChunk = 2048;  // values a block; chunks are numbered in 31 bits
+constexpr int64_t kTensorMaxValues = int64_t(INT32_MAX) * kAdamWChunk;
 size_t grad_norm_workspace_bytes();
 cudaError_t launch_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, float max_norm, float* out,
                              double* partial, int num_sms, cudaStream_t stream);

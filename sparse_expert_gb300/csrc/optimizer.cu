@@ -32,8 +32,10 @@ namespace {
 constexpr int kBlockThreads = 256;
 constexpr int kScaleBlock = 128;
 constexpr int kChunkValues = kBlockThreads * 8;  // one vector a thread
+static_assert(kChunkValues == kAdamWChunk, "the largest tensor's chunks have numbers");
 // of the gradient norm:
 constexpr int kNormVectors = 4;        // 32-byte vectors a thread of a chunk
+static_assert(kNormVectors * kBlockThreads * 8 >= kAdamWChunk, "and so have its larger chunks here");
 constexpr int kLongShare = 24;         // chunks a resident block beyond which there are more blocks
 constexpr int kClusterThreads = 1024;  // of a block of the one cluster for small lists,
 constexpr int kClusterRounds = 2;      // and its chunks a block
@@ -650,7 +652,7 @@ int fill(List<kCapacity>& list, const moe_adamw_tensor_t* tensors, int n_tensors
     const int chunk =
         norm_threads == 0 ? kChunkValues : kNormVectors * norm_threads * 32 / (s.grad_type == MOE_F32 ? 4 : 2);
     const int64_t more = (s.n + chunk - 1) / chunk;
-    if (chunks + more > INT32_MAX) break;
+    if (chunks + more > INT32_MAX) break;  // not at the list's first: kTensorMaxValues
     ++*at;
     if (s.n == 0) continue;
     list.first[list.count] = static_cast<int>(chunks);

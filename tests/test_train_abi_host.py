@@ -97,6 +97,13 @@ def test_adamw_records(status, bad):
     assert lib.moe_adamw_step(record(**bad), 1, HOST, None, None, None) == status
 
 
+@pytest.mark.parametrize("n", [(1 << 42) - 2047, (1 << 42) - 1])
+def test_tensors_of_more_chunks_than_numbers(n):
+    """Refused: such a tensor fits no launch, and the host would look for one without end."""
+    assert lib.moe_adamw_step(record(n=n), 1, HOST, None, None, None) == UNSUPPORTED
+    assert lib.moe_grad_norm(record(n=n), 1, 1.0, FAKE, FAKE, BIG, None) == UNSUPPORTED
+
+
 def test_adamw_arguments():
     r = record()
     assert lib.moe_adamw_step(r, -1, HOST, None, None, None) == INVALID
