@@ -723,7 +723,10 @@ MOE_API moe_status_t moe_router_loss(const float* logits, const int32_t* counts,
  *            out[0] is not finite (a gradient beyond about 1e19 counts as
  *            infinite).  max_norm = infinity: never clipped.
  *   Squares are summed in fp32 by each thread and in fp64 over threads, in a
- *   fixed order.  Workspace: moe_grad_norm_workspace_bytes() bytes.
+ *   fixed order.  Supported: n_tensors <= 1,572,864 (384 a launch, whose
+ *   blocks become fewer with the number of launches: beyond 1,920 tensors
+ *   fewer than the SMs hold).  Workspace: moe_grad_norm_workspace_bytes()
+ *   bytes.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
  * ---------------------------------------------------------------------- */

@@ -231,6 +231,8 @@ size_t moe_grad_norm_workspace_bytes(void) { return grad_norm_workspace_bytes();
 
 moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int32_t n_tensors, float max_norm, float* out,
                            void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (n_tensors > kGradNormMaxTensors)
+    return fail(MOE_ERR_UNSUPPORTED, "n_tensors must be at most 1,572,864 for the gradient norm");
   moe_status_t s = check_list(tensors, n_tensors, false);
   if (s != MOE_OK) return s;
   if (!(max_norm > 0.0f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be positive (infinity: no clipping)");

@@ -290,7 +290,9 @@ size_t router_loss_workspace_bytes();
 cudaError_t launch_router_loss(const RouterLoss& a, int num_sms, cudaStream_t stream);
 
 // The optimizer's lists of tensors (arrays in host memory).
+constexpr int kListMost = 384;  // records that a launch's parameters hold
 constexpr int kGradNormMaxBlocks = 4096;
+constexpr int kGradNormMaxTensors = kGradNormMaxBlocks * kListMost;  // a block for each launch
 constexpr int kAdamWChunk = 2048;  // values a block; chunks are numbered in 31 bits
 constexpr int64_t kTensorMaxValues = int64_t(INT32_MAX) * kAdamWChunk;
 size_t grad_norm_workspace_bytes();

@@ -728,7 +728,7 @@ cudaError_t norm_all(const moe_adamw_tensor_t* tensors, int n_tensors, float max
 // Capacities of the kernels' lists: a call takes the smallest that holds its
 // tensors (a launch copies the whole list), and as many launches of the
 // largest as a longer list needs.
-constexpr int kSmallList = 8, kMediumList = 48, kLargeList = 384;
+constexpr int kSmallList = 8, kMediumList = 48, kLargeList = kListMost;
 static_assert(sizeof(List<kLargeList>) <= 32764, "kernel parameters");
 
 }  // namespace

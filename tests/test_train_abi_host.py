@@ -128,6 +128,13 @@ def test_grad_norm_arguments():
     assert lib.moe_grad_norm(record(n=-5), 1, inf, FAKE, FAKE, BIG, None) == INVALID
 
 
+def test_grad_norm_of_more_tensors_than_partial_sums():
+    """A launch takes up to 384 tensors and needs a partial sum of its own."""
+    n = 4096 * 384 + 1
+    empty = (lib_mod.AdamWTensor * n)()
+    assert lib.moe_grad_norm(empty, n, 1.0, FAKE, FAKE, BIG, None) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("bad", [dict(lr=-1e-3), dict(lr=math.nan), dict(lr=math.inf), dict(b1=1.0), dict(b1=-0.1),
                                  dict(b2=1.0), dict(b2=math.nan), dict(eps=-1.0), dict(wd=math.inf), dict(step=0)])
 def test_adamw_hyper_arguments(bad):
