@@ -63,6 +63,8 @@ class Block:
         packed = moe.moe_pack_weights(p["w_gate"], p["w_up"], p["w_down"])
         ws = torch.empty(moe.moe_forward_workspace_bytes(T, E, k, d, f), dtype=torch.uint8, device="cuda")
         y = moe.moe_forward(n, logits, packed, E, k, f, cfg.renormalize, workspace=ws)
+        # of every routed row: padded tokens take their place at the experts too, so the balance loss counts them in
+        # the load (not in the probabilities that it weighs by it)
         counts = moe.forward_intermediates(ws, T, E, k, d, f)["counts"]
         diff = stream.float() + y.float() - target.float()
         if mask is not None:

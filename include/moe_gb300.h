@@ -658,9 +658,15 @@ MOE_API moe_status_t moe_layer_norm_backward(const void* dy, int64_t dy_stride, 
  * the shares held fixed (they count a discrete choice), so
  *   d[t, e] = p[t, e] / N * (balance_coef E (share_e - sum_i p[t, i] share_i)
  *                            + 2 z_coef lse_t).
- *   logits [T, E] fp32; counts [E] int32 as moe_dispatch_scan writes them
- *   (all zero: every share is zero); mask [T] bytes, optional: tokens whose
- *   byte is 0 are left out (their logits are not read) and get no gradient;
+ *   logits [T, E] fp32; counts [E] int32, the tokens that each expert
+ *   received (all zero: every share is zero).  The mask does not change them:
+ *   as moe_dispatch_scan and moe_forward write them they are of every routed
+ *   row, masked rows too, and losses[0] then weighs the kept tokens'
+ *   probabilities by the load that the experts carry with the padding.  For
+ *   the balance of the kept tokens alone, give the counts of their rows of
+ *   topk_idx;
+ *   mask [T] bytes, optional: tokens whose byte is 0 are left out (their
+ *   logits are not read) and get no gradient;
  *   d_in [T, E] fp32, optional, may be d_logits itself: the gradient that
  *   is added to (moe_backward's d_logits); d_logits [T, E] fp32 out;
  *   losses [2] fp32 out, without the coefficients.

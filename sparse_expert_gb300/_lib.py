@@ -887,8 +887,10 @@ def moe_router_loss(logits, counts, balance_coef=0.01, z_coef=0.001, mask=None, 
     """(losses [2], d_logits [T,E]) of the router's load-balancing loss and
     z-loss (both without their coefficients) and the gradient of
     balance_coef * losses[0] + z_coef * losses[1].
-    counts [E] int32: the tokens each expert received; mask [T] bool: tokens
-    to count; accumulate: a [T,E] gradient that this one is added to, in
+    counts [E] int32: the tokens each expert received, masked ones too where
+    the caller routed and counted them (the mask does not change counts: for
+    the balance of kept tokens alone, count their rows of topk_idx); mask [T]
+    bool: tokens that the means are taken over; accumulate: a [T,E] gradient that this one is added to, in
     place (moe_backward's d_logits)."""
     if stream is not None:
         with torch.cuda.stream(stream):

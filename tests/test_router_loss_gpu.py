@@ -138,6 +138,28 @@ def test_masked_rows_are_not_read_and_get_no_gradient(moe):
     assert torch.equal(after[~mask], before[~mask])
 
 
+@pytest.mark.parametrize("T,E,k", [(300, 16, 2), (5001, 384, 8)])
+def test_counts_decide_which_rows_make_the_shares(moe, T, E, k):
+    """Counts of the kept rows: the losses and gradients of those rows alone.
+    Counts of all routed rows: the kept rows against the load with the others."""
+    logits, _, mask = inputs(T, E, seed=T)
+    topk = torch.topk(logits, k, 1).indices
+
+    def counted(rows):
+        return torch.bincount(topk[rows].flatten(), minlength=E).to(torch.int32)
+    every, kept = counted(torch.ones_like(mask)), counted(mask)
+    assert not torch.equal(every, kept)
+    _, d = check(moe, logits, kept, mask)
+    _, _, tol_l, tol_d = reference(logits[mask], kept, 0.02, 0.003)
+    alone = moe.moe_router_loss(logits[mask], kept, 0.02, 0.003)
+    assert torch.all((moe.moe_router_loss(logits, kept, 0.02, 0.003, mask=mask)[0] - alone[0]).abs() <= 2 * tol_l)
+    assert torch.all((d[mask] - alone[1]).abs() <= 2 * tol_d)
+    with_all, _ = check(moe, logits, every, mask)
+    p = torch.softmax(logits[mask].double(), 1).mean(0)
+    want = E * (p * every.double() / (T * k)).sum()
+    assert abs(with_all[0].item() - want.item()) <= 1e-5 * want.item()
+
+
 def test_nothing_kept(moe):
     logits, counts, _ = inputs(77, 24, seed=11)
     none = torch.zeros(77, dtype=torch.bool, device="cuda")
