@@ -301,6 +301,31 @@ def test_same_bits_every_time_and_on_another_stream(moe, T, d):
         assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("T,d", [(20, 128), (2503, 6144), (777, 1001), (40, 30000)])
+def test_graph_replay(moe, T, d):
+    """Forward and backward in one captured graph, replayed on other inputs."""
+    x, r, dy = (rows(T, d, torch.bfloat16, seed=s) for s in (1, 2, 3))
+    w, b = params(d, torch.float32, seed=4)
+    y, z, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(2, T, device="cuda")
+    grads = dict(dx=torch.empty_like(x), dweight=torch.empty_like(w), dbias=torch.empty_like(b))
+    ws = torch.empty(moe.moe_layer_norm_backward_workspace_bytes(T, d), dtype=torch.uint8, device="cuda")
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            moe.moe_layer_norm(x, w, b, residual=r, out=y, stats=stats, z=z, stream=stream)
+            moe.moe_layer_norm_backward(dy, z, stats, w, dz=r, grads=grads, workspace=ws, stream=stream)
+    for seed in (5, 6):
+        for t in (x, r, dy):
+            t.copy_(rows(T, d, torch.bfloat16, seed=seed))
+        graph.replay()
+        want = moe.moe_layer_norm(x, w, b, residual=r)
+        want_grads = moe.moe_layer_norm_backward(dy, want[2], want[1], w, dz=r)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip((y, stats, z), want))
+        assert all(torch.equal(grads[k], want_grads[k]) for k in grads)
+
+
 def test_offsets_beyond_32_bits(moe):
     """Rows whose element offsets pass 2^32: the last rows are right."""
     T, d = 9, 1 << 29

@@ -102,6 +102,50 @@ def test_more_pieces_than_blocks(moe, T, E):
         assert all(torch.equal(p, q) for p, q in zip(first, again))
 
 
+@pytest.mark.parametrize("T,E", [(100, 64), (100, 33), (9001, 384), (22003, 384), (30001, 8)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_gradient_added_to_one_that_stays(moe, T, E, masked):
+    """d_in apart from d_logits: read and not written; masked rows are copies of it."""
+    logits, counts, mask = inputs(T, E, seed=T + E)
+    mask = mask if masked else None
+    d_in = torch.randn(T, E, device="cuda") * 1e-4
+    kept = d_in.clone()
+    d, losses = torch.full_like(logits, float("nan")), torch.empty(2, device="cuda")
+    ws = torch.empty(moe._lib.lib.moe_router_loss_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    assert moe._lib.lib.moe_router_loss(ptr(logits), ptr(counts), ptr(mask), T, E, 0.02, 0.003, ptr(d_in), ptr(d),
+                                        ptr(losses), ptr(ws), ws.numel(),
+                                        torch.cuda.current_stream().cuda_stream) == 0
+    want_l, want_d, tol_l, tol_d = reference(logits, counts, 0.02, 0.003, mask, d_in)
+    assert torch.equal(d_in, kept) and torch.all((d.double() - want_d).abs() <= tol_d)
+    assert torch.all((losses.double() - want_l).abs() <= tol_l)
+    if masked:
+        assert torch.equal(d[~mask], d_in[~mask])
+
+
+@pytest.mark.parametrize("T,E", [(100, 64), (9001, 384), (22003, 384)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_graph_replay(moe, T, E, masked):
+    logits, counts, mask = inputs(T, E, seed=3)
+    mask = mask if masked else None
+    out, losses = torch.empty_like(logits), torch.empty(2, device="cuda")
+    ws = torch.empty(moe._lib.lib.moe_router_loss_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            moe.moe_router_loss(logits, counts, mask=mask, out=out, losses=losses, workspace=ws, stream=stream)
+    for seed in (4, 5):
+        new, new_counts, new_mask = inputs(T, E, seed=seed)
+        logits.copy_(new), counts.copy_(new_counts)
+        if masked:
+            mask.copy_(new_mask)
+        graph.replay()
+        want_l, want_d = moe.moe_router_loss(new, new_counts, mask=new_mask if masked else None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want_d) and torch.equal(losses, want_l)
+
+
 def test_unaligned_rows(moe):
     buf = torch.randn(200 * 64 + 1, device="cuda")
     logits = buf[1:].view(200, 64)
