@@ -31,7 +31,9 @@ constexpr int kForwardStages = kChunks == 1 ? 6 : kChunks == 3 ? 4 : 3;
 // Bound by memory: 64k x 6144 bf16 with a residual 466 us = 6.9 TB/s, 64k x
 // 2048 without 81 us = 6.6 TB/s.  Rows that do not start on a chunk keep
 // fixed shares and checks of their ends, and are bound by their instructions:
-// 34,462 x 3,570 fp16 with a residual 213 us = 4.6 TB/s.
+// 34,462 x 3,570 fp16 with a residual 216 us = 4.6 TB/s.  The reciprocal root
+// is the approximate one, right to two units in the last place of fp32, which
+// the variance's own sum leaves too.
 template <typename T, int kChunks, Fit kFit, int kTpr>
 __global__ void __launch_bounds__(kRingThreads, 1) forward_ring_kernel(const ForwardArgs a) {
   constexpr int P = kPairs<T>, S = kForwardStages<kChunks>, B = kBatch<kChunks>;
@@ -305,8 +307,9 @@ __global__ void __launch_bounds__(1024) forward_values_kernel(const ForwardArgs 
 
 // Rows beyond the rings, one block a row in three sweeps (mean, deviations,
 // output): bound by the two exchanges a row, between which a block reads
-// nothing, and where a row's start allows single values only (kVec false) by
-// its instructions (4,000 x 15,001 fp32: 228 us = 2.1 TB/s).  `cached`: the
+// nothing (8,192 x 32,768 bf16: 299 us = 3.6 TB/s, with a residual 395 us = 5.4
+// TB/s), and where a row's start allows single values only (kVec false) by its
+// instructions (4,000 x 15,001 fp32: 231 us = 2.1 TB/s).  `cached`: the
 // row stays in shared memory between sweeps, else they read it again.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(1024) forward_long_kernel(const ForwardArgs a, bool cached) {

@@ -17,8 +17,10 @@
 //
 // Bound by memory with 32-bit states (403M bf16 weights with masters 1589 us =
 // 7.1 TB/s) and with 8-bit states and masters (528M: 1248 us = 6.8 TB/s); with
-// 8-bit states alone, 60-70 instructions a value bind it (202M: 392 us = 5.2
-// TB/s).
+// 8-bit states alone, 62 instructions a value bind it, in 85 % of the issue
+// slots (202M: 392 us = 5.2 TB/s).  Some of them are spills: the kernel for
+// 8-bit states holds all forms of a chunk in 40 registers, and its threads
+// store 212 and load 308 bytes of them in the worst case.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -436,6 +438,9 @@ __device__ __forceinline__ void adamw_last_chunk(const Tensor& t, const moe_adam
 
 // A chunk of a tensor whose pointers are not all at 32-byte boundaries: a warp
 // takes blocks of 128 values, lane + 32 i of each, in accesses of one value.
+// Tensors with allocations of their own never come here.  Bound by the number
+// of its accesses (50M bf16 weights with masters: 451 us where vectors take
+// 204, with 8-bit states 406 and 123).
 __device__ __forceinline__ void adamw_scalar_chunk(const Tensor& t, const moe_adamw_hyper_t& h, const float* factor_p,
                                                    int64_t begin) {
   const float factor = factor_p ? *factor_p : 1.0f;
