@@ -40,6 +40,8 @@
  *     word at the start of the workspace and read back with
  *     moe_get_device_status or moe_read_device_status.
  *   - Calls that share a workspace must not overlap on the GPU.
+ *   - The forms for a few tokens and the 4-bit weights have sizes of their
+ *     own, given with them.
  *   - The training-step operators (layer norm, router losses, gradient norm,
  *     AdamW) take other element types, row strides and any d: see each.
  *   - Supported sizes: 1 <= E <= 1024, 1 <= k <= min(E, 32), 0 <= T,
@@ -468,6 +470,90 @@ MOE_API moe_status_t moe_forward_routed(const void* x, const void* router_packed
                                 int32_t renormalize, void* out,
                                 int32_t* topk_idx_out, float* topk_w_out,
                                 void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS), the form of a
+ * serving step: two launches, the time that of reading the weights of the
+ * experts that some token chose (the other experts' are not read).
+ *   moe_forward_few         routes by logits [T, E] fp32, as moe_forward;
+ *   moe_forward_few_routed  by x and moe_pack_router_weights' weights (E <= 512,
+ *                           16-byte aligned): fp32 logits, within 2e-7 of the
+ *                           largest partial sums.
+ *   x [T, d] bf16; out [T, d] bf16 out; renormalize, topk_idx_out and
+ *   topk_w_out (both optional) as moe_forward.  Selection, ties and gates are
+ *   moe_route_topk's.
+ *   weights  the experts' weights as one of
+ *     MOE_WEIGHTS_BF16  moe_pack_weights' layout;
+ *     MOE_WEIGHTS_FP8   moe_pack_weights_fp8's (d and f multiples of 128; codes
+ *                       finite).  The weight is E4M3 value x scale, not rounded
+ *                       to bf16 on the way (moe_forward_fp8 does): the scale is
+ *                       multiplied into the inputs instead, and those products
+ *                       are rounded to bf16;
+ *     MOE_WEIGHTS_INT4  moe_pack_weights_int4's with the same `group` (d and f
+ *                       multiples of 128).  The weight is (code - 8) x scale;
+ *                       codes are multiplied exactly, scales enter in fp32.
+ *   group    of 4-bit weights; not looked at for the others.
+ * h = silu(gate) * up is rounded to bf16, as everywhere in the layer; sums,
+ * gates and the experts' outputs stay fp32 until out is rounded.  Results are
+ * the same bits every time.  Logits must be finite (an expert with a logit of
+ * -infinity is not chosen while k others are finite).
+ * moe_forward_few_workspace_bytes gives 0 for sizes outside the range.  A
+ * wait that ran out sets MOE_ERR_TIMEOUT in the workspace's status word.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
+ *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+#define MOE_FEW_MAX_TOKENS 64
+typedef enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_FP8 = 1, MOE_WEIGHTS_INT4 = 2 } moe_weights_t;
+
+MOE_API size_t moe_forward_few_workspace_bytes(int64_t T, int32_t E, int32_t k, int32_t d, int32_t f);
+MOE_API moe_status_t moe_forward_few(const void* x, const float* logits, const void* packed, int32_t weights,
+                                     int32_t group, int64_t T, int32_t d, int32_t E, int32_t k, int32_t f,
+                                     int32_t renormalize, void* out, int32_t* topk_idx_out, float* topk_w_out,
+                                     void* workspace, size_t workspace_bytes, moe_stream_t stream);
+MOE_API moe_status_t moe_forward_few_routed(const void* x, const void* router_packed, const void* packed,
+                                            int32_t weights, int32_t group, int64_t T, int32_t d, int32_t E,
+                                            int32_t k, int32_t f, int32_t renormalize, void* out,
+                                            int32_t* topk_idx_out, float* topk_w_out, void* workspace,
+                                            size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit weights with group scales.  A matrix [K, N] (y = x @ w) is held as
+ *   codes  [K/2, N] uint8: the code 0 .. 15 of input 2i in the low half of
+ *          byte (i, n), that of input 2i + 1 in the high half;
+ *   scales [ceil(K / group), N] bf16: one for `group` consecutive inputs of an
+ *          output (32, 64 or 128; the last group may be shorter);
+ * and its weights are (code - 8) x scale.  K is a multiple of 8 up to 65536,
+ * N any up to 2^24.
+ * moe_quantize_int4: codes and scales of `matrices` matrices [K, N] of bf16,
+ *   one after the other.  scale = bf16(amax / 7) (1 where that is 0), code =
+ *   8 + w / scale rounded to nearest even, within 0 .. 15.
+ * moe_pack_weights_int4: experts' codes and scales (gate, up: [E] matrices
+ *   [d, f]; down: [f, d]; d and f multiples of 128) in the layout that
+ *   moe_forward_few reads, moe_int4_packed_weight_bytes(E, d, f, group) bytes,
+ *   256-byte aligned.
+ * moe_pack_linear_int4, moe_linear_int4: one matrix, packed once into
+ *   moe_linear_int4_packed_bytes(K, N, group) bytes (256-byte aligned), and
+ *   its product with a few rows:
+ *     out[m, :] = bf16(x[m, :] @ w),  0 <= M <= MOE_LINEAR_INT4_MAX_ROWS,
+ *   x [M, K] bf16 with x_stride values between rows (rows 16-byte aligned),
+ *   out [M, N] bf16 with out_stride.  Codes are multiplied exactly, sums and
+ *   scales are fp32, out is rounded once.  The same bits every time.
+ * The sizes are 0 outside the range.  Errors: MOE_ERR_INVALID_ARG,
+ * MOE_ERR_UNSUPPORTED, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+#define MOE_LINEAR_INT4_MAX_ROWS 16
+MOE_API moe_status_t moe_quantize_int4(const void* w, int64_t matrices, int64_t K, int64_t N, int32_t group,
+                                       uint8_t* codes, void* scales, moe_stream_t stream);
+MOE_API size_t moe_int4_packed_weight_bytes(int32_t E, int32_t d, int32_t f, int32_t group);
+MOE_API moe_status_t moe_pack_weights_int4(const uint8_t* gate_codes, const void* gate_scales,
+                                           const uint8_t* up_codes, const void* up_scales, const uint8_t* down_codes,
+                                           const void* down_scales, int32_t E, int32_t d, int32_t f, int32_t group,
+                                           void* packed, moe_stream_t stream);
+MOE_API size_t moe_linear_int4_packed_bytes(int64_t K, int64_t N, int32_t group);
+MOE_API moe_status_t moe_pack_linear_int4(const uint8_t* codes, const void* scales, int64_t K, int64_t N,
+                                          int32_t group, void* packed, moe_stream_t stream);
+MOE_API moe_status_t moe_linear_int4(const void* x, int64_t x_stride, const void* packed, int64_t M, int64_t K,
+                                     int64_t N, int32_t group, void* out, int64_t out_stride, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The whole layer backward: the gradients of moe_forward's output with

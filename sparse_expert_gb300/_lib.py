@@ -122,6 +122,16 @@ SIGNATURES = {
     "moe_adamw_step": (_S, [_P, _I32, _P, _P, _P, _P]),
     "moe_grad_norm_workspace_bytes": (_SZ, []),
     "moe_grad_norm": (_S, [_P, _I32, _F, _P, _P, _SZ, _P]),
+    "moe_forward_few_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "moe_forward_few": (_S, [_P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "moe_forward_few_routed": (_S, [_P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ,
+                                    _P]),
+    "moe_quantize_int4": (_S, [_P, _I64, _I64, _I64, _I32, _P, _P, _P]),
+    "moe_int4_packed_weight_bytes": (_SZ, [_I32, _I32, _I32, _I32]),
+    "moe_pack_weights_int4": (_S, [_P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_linear_int4_packed_bytes": (_SZ, [_I64, _I64, _I32]),
+    "moe_pack_linear_int4": (_S, [_P, _P, _I64, _I64, _I32, _P, _P]),
+    "moe_linear_int4": (_S, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)
@@ -1105,3 +1115,188 @@ def moe_adamw_step(plan, lr=None, step=None, betas=(0.9, 0.95), eps=1e-8, weight
                                 _raw_stream(index) if stream is None else stream.cuda_stream)
     if status:
         _check(status, "moe_adamw_step")
+
+
+# ------------------------------------- the layer for a few tokens, 4-bit weights
+FEW_MAX_TOKENS = 64
+LINEAR_INT4_MAX_ROWS = 16
+_WEIGHTS = {"bf16": 0, "fp8": 1, "int4": 2}  # moe_weights_t
+
+
+@functools.lru_cache(maxsize=256)
+def moe_forward_few_workspace_bytes(T, E, k, d, f) -> int:
+    """Bytes of a workspace; 0 for sizes outside the range."""
+    return lib.moe_forward_few_workspace_bytes(T, E, k, d, f)
+
+
+@functools.lru_cache(maxsize=256)
+def _packed_bytes(weights, E, d, f, group) -> int:
+    if weights == "bf16":
+        return lib.moe_packed_weight_bytes(E, d, f)
+    return lib.moe_fp8_packed_weight_bytes(E, d, f) if weights == "fp8" else \
+        lib.moe_int4_packed_weight_bytes(E, d, f, group)
+
+
+def _bytes_at_least(t, index, size, name):
+    """A contiguous uint8 buffer on device `index` with `size` bytes or more."""
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        _contig(t, torch.uint8, name)
+    if t.numel() < size:
+        raise ValueError(f"{name} has {t.numel()} bytes, these sizes need {size}")
+    return t.data_ptr()
+
+
+def _forward_few(entry, where, x, route, route_ptr, packed, E, k, f, weights, group, renormalize, workspace, out,
+                 topk_idx, topk_w, index):
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _contig(x, torch.bfloat16, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, d], got {list(shape)}")
+    T, d = shape
+    kind = _WEIGHTS.get(weights)
+    if kind is None:
+        raise ValueError(f"weights must be one of {sorted(_WEIGHTS)}, got {weights!r}")
+    p_ptr = _bytes_at_least(packed, index, _packed_bytes(weights, E, d, f, group), "packed")
+    dev = x.device
+    if workspace is None:
+        size = moe_forward_few_workspace_bytes(T, E, k, d, f)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    else:
+        size = _workspace(workspace, index)
+    out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else \
+        _out(out, index, shape, torch.bfloat16, "out")
+    i_ptr = None if topk_idx is None else _out(topk_idx, index, (T, k), torch.int32, "topk_idx").data_ptr()
+    w_ptr = None if topk_w is None else _out(topk_w, index, (T, k), torch.float32, "topk_w").data_ptr()
+    status = entry(x.data_ptr(), route_ptr, p_ptr, kind, group, T, d, E, k, f, 1 if renormalize else 0, out.data_ptr(),
+                   i_ptr, w_ptr, workspace.data_ptr(), size, _raw_stream(index))
+    if status:
+        _check(status, where)
+    return out
+
+
+def moe_forward_few(x, logits, packed, E, k, f, weights="bf16", group=128, renormalize=True, workspace=None, out=None,
+                    topk_idx=None, topk_w=None, stream=None):
+    """out [T,d] of the whole layer for T <= 64 tokens, routed by logits [T,E].
+    weights: "bf16" (packed by moe_pack_weights), "fp8" (moe_pack_weights_fp8) or
+    "int4" (moe_pack_weights_int4, with the same group); topk_idx, topk_w
+    [T,k]: written where given."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_forward_few(x, logits, packed, E, k, f, weights, group, renormalize, workspace, out, topk_idx,
+                                   topk_w)
+    index = _device_of(x, "x")
+    _out(logits, index, (x.shape[0], E), torch.float32, "logits")
+    return _forward_few(lib.moe_forward_few, "moe_forward_few", x, logits, logits.data_ptr(), packed, E, k, f, weights,
+                        group, renormalize, workspace, out, topk_idx, topk_w, index)
+
+
+def moe_forward_few_routed(x, router_packed, packed, E, k, f, weights="bf16", group=128, renormalize=True,
+                           workspace=None, out=None, topk_idx=None, topk_w=None, stream=None):
+    """moe_forward_few from the router's weights (packed by moe_pack_router_weights)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_forward_few_routed(x, router_packed, packed, E, k, f, weights, group, renormalize, workspace,
+                                          out, topk_idx, topk_w)
+    index = _device_of(x, "x")
+    r_ptr = _bytes_at_least(router_packed, index, _router_bytes(x.shape[-1], E), "router_packed")
+    return _forward_few(lib.moe_forward_few_routed, "moe_forward_few_routed", x, router_packed, r_ptr, packed, E, k, f,
+                        weights, group, renormalize, workspace, out, topk_idx, topk_w, index)
+
+
+@functools.lru_cache(maxsize=256)
+def _router_bytes(d, E) -> int:
+    return lib.moe_router_packed_bytes(d, E)
+
+
+def moe_quantize_int4(w, group=128, stream=None):
+    """(codes uint8 [..., K/2, N], scales bf16 [..., ceil(K/group), N]) of bf16 weights w [..., K, N]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_quantize_int4(w, group)
+    index = _device_of(w, "w")
+    _contig(w, torch.bfloat16, "w")
+    if w.dim() < 2:
+        raise ValueError(f"w must be [..., K, N], got {list(w.shape)}")
+    *lead, K, N = w.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    n = 1
+    for m in lead:
+        n *= m
+    codes = torch.empty(*lead, K // 2, N, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(*lead, -(-K // group), N, dtype=torch.bfloat16, device=w.device)
+    _check(lib.moe_quantize_int4(w.data_ptr(), n, K, N, group, codes.data_ptr(), scales.data_ptr(), _raw_stream(index)),
+           "moe_quantize_int4")
+    return codes, scales
+
+
+def _int4_operands(codes, scales, index, lead, K, N, group, name):
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    _out(codes, index, (*lead, K // 2, N), torch.uint8, f"{name} codes")
+    _out(scales, index, (*lead, -(-K // group), N), torch.bfloat16, f"{name} scales")
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def moe_int4_packed_weight_bytes(E, d, f, group=128) -> int:
+    return lib.moe_int4_packed_weight_bytes(E, d, f, group)
+
+
+def moe_pack_weights_int4(gate, up, down, E, d, f, group=128, stream=None):
+    """4-bit expert weights (uint8 buffer) for moe_forward_few from three (codes, scales) pairs as moe_quantize_int4
+    returns them for w_gate, w_up [E,d,f] and w_down [E,f,d]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_pack_weights_int4(gate, up, down, E, d, f, group)
+    index = _device_of(gate[0], "gate codes")
+    ptrs = []
+    for (codes, scales), K, N, name in ((gate, d, f, "gate"), (up, d, f, "up"), (down, f, d, "down")):
+        ptrs += _int4_operands(codes, scales, index, (E,), K, N, group, name)
+    packed = torch.empty(lib.moe_int4_packed_weight_bytes(E, d, f, group), dtype=torch.uint8, device=gate[0].device)
+    _check(lib.moe_pack_weights_int4(*ptrs, E, d, f, group, packed.data_ptr() or 256, _raw_stream(index)),
+           "moe_pack_weights_int4")
+    return packed
+
+
+def moe_linear_int4_packed_bytes(K, N, group=128) -> int:
+    return lib.moe_linear_int4_packed_bytes(K, N, group)
+
+
+_linear_int4_bytes = functools.lru_cache(maxsize=256)(moe_linear_int4_packed_bytes)
+
+
+def moe_pack_linear_int4(codes, scales, K, N, group=128, stream=None):
+    """A 4-bit matrix [K,N] (uint8 buffer) for moe_linear_int4 from codes [K/2,N] and scales [ceil(K/group),N]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_pack_linear_int4(codes, scales, K, N, group)
+    index = _device_of(codes, "codes")
+    ptrs = _int4_operands(codes, scales, index, (), K, N, group, "the matrix's")
+    packed = torch.empty(lib.moe_linear_int4_packed_bytes(K, N, group), dtype=torch.uint8, device=codes.device)
+    _check(lib.moe_pack_linear_int4(*ptrs, K, N, group, packed.data_ptr() or 256, _raw_stream(index)),
+           "moe_pack_linear_int4")
+    return packed
+
+
+def moe_linear_int4(x, packed, N, group=128, out=None, stream=None):
+    """out [M,N] bf16 = x [M,K] bf16 (rows 16-byte aligned, any stride) times a matrix packed by moe_pack_linear_int4,
+    M <= 16.  out: [M,N] with unit stride along N, any row stride."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_linear_int4(x, packed, N, group, out)
+    index = _device_of(x, "x")
+    x_stride = _rows(x, "x", index, None, torch.bfloat16)
+    M, K = x.shape
+    if out is None:
+        out, out_stride = torch.empty((M, N), dtype=torch.bfloat16, device=x.device), N
+    else:
+        out_stride = _rows(out, "out", index, (M, N), torch.bfloat16)
+    p_ptr = _bytes_at_least(packed, index, _linear_int4_bytes(K, N, group), "packed")
+    status = lib.moe_linear_int4(x.data_ptr(), x_stride, p_ptr, M, K, N, group, out.data_ptr(), out_stride,
+                                 _raw_stream(index))
+    if status:
+        _check(status, "moe_linear_int4")
+    return out

@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["abi.cu", "route.cu", "router.cu", "dispatch.cu", "dispatch_noalloc.cu", "permute_combine.cu", "pack.cu",
            "grouped_gemm.cu", "fp8.cu", "backward.cu", "tensor_map.cu", "grouped_gemm_bwd.cu",
            "selftest.cu", "grouped_gemm_2sm.cu", "layer_norm.cu",
-           "layer_norm_f32.cu", "layer_norm_bf16.cu", "layer_norm_f16.cu", "router_loss.cu", "optimizer.cu", "abi_train.cu"]
+           "layer_norm_f32.cu", "layer_norm_bf16.cu", "layer_norm_f16.cu", "router_loss.cu", "optimizer.cu", "abi_train.cu",
+           "few_route.cu", "few.cu", "int4.cu", "linear_int4.cu", "abi_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3,-Wall,-fvisibility=hidden", "--expt-relaxed-constexpr",
           "-I", os.path.join(ROOT, "include"), "-I", CSRC]

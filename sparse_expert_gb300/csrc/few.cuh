@@ -1,0 +1,51 @@
+// The layer for a few tokens (T <= 64): what its kernels share.
+//
+// A unit is one expert with up to kFewChunk of the tokens routed to it.  The
+// route kernel turns the top-k selection into the list of units; everything
+// after it goes by units, so an expert that no token chose costs nothing.
+// The rows of a unit (one for each of its tokens, in token order) are
+// consecutive in the buffers h and y.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kFewMaxTokens = 64;  // a set of tokens is a 64-bit mask
+constexpr int kFewStrip = 32;      // output features that finished units are counted for
+constexpr int kFewChunk = 16;      // tokens of a unit: two 8-column tiles of the matrix instructions
+
+struct FewUnit {
+  int32_t expert;
+  int32_t row;      // of the unit's first token
+  uint64_t tokens;  // bit t: token t
+};
+
+// Lies over the workspace's header.
+struct FewHeader {
+  int32_t status;
+  int32_t n_units;
+  int32_t ticket;  // next piece of work of the expert kernel
+  int32_t unused[61];
+};
+static_assert(sizeof(FewHeader) == sizeof(WsHeader), "the status word and the header's size are shared");
+
+__device__ __forceinline__ int few_rank(uint64_t tokens, int t) {
+  return __popcll(tokens & ((uint64_t(1) << t) - 1));
+}
+
+// D += A B on the tensor cores: A 16 x 16 (rows g and g + 8 of lane 4g + t),
+// B 16 x 8 (column g), bf16, D fp32 (columns 2t and 2t + 1 of both rows).
+// The order of the 16 inner indices is free as long as A and B agree.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+}  // namespace moe

@@ -301,6 +301,62 @@ cudaError_t launch_grad_norm(const moe_adamw_tensor_t* tensors, int n_tensors, f
 cudaError_t launch_adamw(const moe_adamw_tensor_t* tensors, int n_tensors, const moe_adamw_hyper_t* hyper,
                          const moe_adamw_hyper_t* hyper_dev, const float* grad_scale, cudaStream_t stream);
 
+// ---- the layer for a few tokens
+struct FewUnit;
+struct FewHeader;
+struct FewRoute {
+  const void* x;         // [T, d] bf16; read with router weights only
+  const void* router;    // moe_pack_router_weights' layout, or null
+  const float* logits;   // [T, E], without router weights
+  float* logits_out;     // [T, E], with them
+  int T, d, E, E_pad, k, renormalize;
+  int32_t* topk_idx;     // [T, k]
+  float* topk_w;         // [T, k]
+  int32_t* pair_row;     // [T, k] out: row of the pair in h and y
+  FewUnit* units;        // out
+  FewHeader* header;     // out: status and ticket cleared, number of units
+  int32_t* counters;     // out: cleared
+  int n_counters;
+};
+cudaError_t launch_few_route(const FewRoute& p, cudaStream_t stream);
+struct FewExperts {
+  const void* x;         // [T, d] bf16
+  const void* packed;    // in the layout of `weights`
+  int weights, group;    // moe_weights_t; of int4
+  int T, d, E, k, f;
+  const FewUnit* units;
+  FewHeader* header;
+  int32_t* ready;        // for each unit: finished strips of h
+  int32_t* strips;       // for each strip of outputs: finished units
+  const float* topk_w;
+  const int32_t* pair_row;
+  void* h;               // [T*k, f] bf16
+  float* y;              // [T*k, d]
+  void* out;             // [T, d] bf16
+};
+cudaError_t launch_few_experts(const FewExperts& p, int num_sms, cudaStream_t stream);
+
+// ---- 4-bit weights: codes 0 .. 15 of (code - 8) x scale, one bf16 scale for
+// `group` inputs of an output feature.  Layout: strips of kInt4Rows output
+// features (gate/up: kInt4Rows / 2 gate features, then the same up features),
+// each a row of records of kInt4Unit inputs; see int4.cuh.
+size_t int4_matrix_bytes(int64_t matrices, int K, int64_t N, int group);
+cudaError_t launch_quantize_int4(const void* w, int64_t matrices, int64_t K, int64_t N, int group, uint8_t* codes,
+                                 void* scales, int num_sms, cudaStream_t stream);
+// `up` null: one projection [matrices][K][N]; else gate and up, interleaved.
+cudaError_t launch_pack_int4(const uint8_t* codes, const void* scales, const uint8_t* up_codes, const void* up_scales,
+                             int64_t matrices, int K, int N, int group, void* packed, int num_sms,
+                             cudaStream_t stream);
+struct LinearInt4 {
+  const void* x;  // [M] rows of K bf16
+  int64_t x_stride;
+  const void* packed;
+  int M, K, N, group;
+  void* out;      // [M] rows of N bf16
+  int64_t out_stride;
+};
+cudaError_t launch_linear_int4(const LinearInt4& p, int num_sms, cudaStream_t stream);
+
 // Bounded-wait check: one block waits on a phase that never completes and
 // records a timeout in *status after limit_ns.
 cudaError_t launch_wait_timeout(int32_t* status, uint64_t limit_ns, cudaStream_t stream);
