@@ -87,7 +87,7 @@ FewLayout few_layout(int64_t T, int32_t E, int32_t k, int32_t d, int32_t f) {
   L.topk_idx = take(sizeof(int32_t) * P);
   L.topk_w = take(sizeof(float) * P);
   L.logits = take(sizeof(float) * static_cast<size_t>(T) * E);
-  L.h = take(size_t(2) * P * f);
+  L.h = take(size_t(4) * P * f);  // high parts, then low parts
   L.y = take(sizeof(float) * P * d);
   L.total = o;
   return L;

@@ -14,14 +14,16 @@
 namespace moe {
 
 constexpr int kFewMaxTokens = 64;  // a set of tokens is a 64-bit mask
-constexpr int kFewStrip = 32;      // output features that finished units are counted for
+constexpr int kFewStrip = 32;      // fewest output features of a piece of the down projection
 constexpr int kFewChunk = 16;      // tokens of a unit: two 8-column tiles of the matrix instructions
 
 struct FewUnit {
-  int32_t expert;
-  int32_t row;      // of the unit's first token
-  uint64_t tokens;  // bit t: token t
+  int16_t expert;
+  int8_t chunk, chunks;  // this one of the expert's units, and how many they are (consecutive in the list)
+  int32_t row;           // of the unit's first token
+  uint64_t tokens;       // bit t: token t
 };
+static_assert(sizeof(FewUnit) == 16, "read as one vector");
 
 // Lies over the workspace's header.
 struct FewHeader {

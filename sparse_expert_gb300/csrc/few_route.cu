@@ -165,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_route_kernel(const FewRoute p
     if (e < p.E) {
       uint64_t rest = tokens_of[e];
       int row = before & 0xffff, u = before >> 16;
+      const int chunks = own[i] >> 16;
       row_of[e] = row;
-      while (rest) {  // kFewChunk tokens at a time
+      for (int c = 0; c < chunks; ++c) {  // kFewChunk tokens at a time
         uint64_t part = 0;
         int n = 0;
         for (; n < kFewChunk && rest; ++n) {
           part |= rest & (~rest + 1);
           rest &= rest - 1;
         }
-        p.units[u++] = FewUnit{e, row, part};
+        p.units[u++] = FewUnit{static_cast<int16_t>(e), static_cast<int8_t>(c), static_cast<int8_t>(chunks), row, part};
         row += n;
       }
     }
