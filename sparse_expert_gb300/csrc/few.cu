@@ -17,14 +17,19 @@
 // earlier by a block that runs, so the wait ends whether or not all blocks are
 // on the GPU at once.
 //
+// Behind them come pieces of the gated sum, which wait for their columns of y.
+//
 // Inside a block, one warp fetches weights (bulk copies into a ring of stages
-// of 512 inner indices), another the tokens' rows for the same stages, and the
-// others multiply: each takes one 64-index block of a stage, for all rows and
-// tokens, and at the end of the strip their sums are added in a fixed order.
-// The weight warp does not wait for h, so the next projection's weights are in
-// flight while the last rows of h are being finished.  The inner indices are
-// split over the warps rather than the rows, because every warp then reads its
-// own part of the tokens' rows once, for all rows of the strip.
+// of 512 inner indices), another the tokens' rows for the same stages into a
+// ring of their own, and the others multiply: each takes one 64-index block of
+// a stage, for all rows and tokens, and at the end of the strip their sums are
+// added in a fixed order.  A last warp tells other blocks of finished strips,
+// which takes about a microsecond of waiting for memory that the multiplying
+// warps so do not spend.  The weight warp does not wait for h: the next
+// projection's weights are in flight while the last rows of h are being
+// finished.  The inner indices are split over the warps rather than the rows,
+// because every warp then reads its own part of the tokens' rows once, for all
+// rows of the strip.
 #include "few.cuh"
 #include "int4.cuh"
 #include "int4_mma.cuh"
@@ -37,6 +42,7 @@ namespace {
 constexpr int kStageKb = 8;                      // 64-index blocks of a stage, one for each warp of a group
 constexpr int kMaxStages = 8;
 constexpr int kItems = 4;                        // pieces between the weight warp and the others
+constexpr int kSumCols = 64, kSumTokens = 8;     // of a piece of the gated sum
 constexpr int kUnitCache = 512;                  // units kept in shared memory
 constexpr size_t kSmemMost = 227 * 1024 - 1024 - sizeof(FewUnit) * kUnitCache;  // less the static variables
 
@@ -67,7 +73,9 @@ struct Args {
   int64_t low_offset;                           // bytes from the high parts of h to the low parts
   int down_bn;                                  // rows of a packed bf16 down tile
   int cap;                                      // token rows of a stage: min(T, 16)
-  int stages, stage_bytes, scale_offset, row_offset, reduce_offset;
+  int stages, stage_bytes, scale_offset;        // weights
+  int row_stages, row_stage_bytes, row_offset;  // tokens' rows
+  int reduce_offset;
 };
 
 __device__ __forceinline__ int32_t load_acquire(const int32_t* p) {
@@ -100,6 +108,21 @@ struct Slot {
     }
   }
 };
+
+// Or-reduction over the multiplying warps, all of which meet here.
+template <int kThreads>
+__device__ __forceinline__ bool any_of(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "n"(kThreads)
+      : "memory");
+  return r != 0;
+}
 
 struct Piece {
   int unit, strip;
@@ -242,15 +265,15 @@ struct Multiply<MOE_WEIGHTS_INT4> {
 };
 
 template <int kKind>
-__global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_experts_kernel(const Args a) {
+__global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_experts_kernel(const Args a) {
   using F = Format<kKind>;
   constexpr int kRows = F::kRows, kTiles = kRows / 16, kWarps = F::kGroups * 8, kThreads = kWarps * 32;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t full_w[kMaxStages], full_x[kMaxStages], empty[kMaxStages];
-  __shared__ uint64_t item_full[kItems], item_empty[kItems];
+  __shared__ uint64_t full_w[kMaxStages], empty_w[kMaxStages], full_x[kMaxStages], empty_x[kMaxStages];
+  __shared__ uint64_t item_full[kItems], item_done[kItems], item_empty[kItems];
   __shared__ int32_t item[kItems];
   __shared__ __align__(16) FewUnit unit_cache[kUnitCache];
-  __shared__ int abort_s, last_s, n_units_s, first_s;
+  __shared__ int abort_s, n_units_s, first_s;
   const FewExperts& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &abort_s;
@@ -258,12 +281,16 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full_w[i], 1);
+      mbar_init(&empty_w[i], 8);
+    }
+    for (int i = 0; i < a.row_stages; ++i) {
       mbar_init(&full_x[i], 1);
-      mbar_init(&empty[i], 8);
+      mbar_init(&empty_x[i], 8);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], 1 + kWarps);
+      mbar_init(&item_done[i], kWarps);
+      mbar_init(&item_empty[i], 2 + kWarps);
     }
     abort_s = 0;
     fence_barrier_init();
@@ -282,7 +309,8 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
   const FewUnit* units = most <= kUnitCache ? unit_cache : p.units;
   const int n_units = n_units_s;
   const int strips1 = 2 * p.f / kRows, strips2 = p.d / kRows;
-  const int total = n_units * (strips1 + strips2);
+  const int products = n_units * (strips1 + strips2);  // pieces
+  const int sum_groups = (p.T + kSumTokens - 1) / kSumTokens, total = products + p.d / kSumCols * sum_groups;
   const int kb1 = p.d / 64, kb2 = p.f / 64;
   constexpr int kPitch = kStageKb * 128 + F::kPad;
   bool ok = true;
@@ -302,11 +330,15 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
       }
       it.next(kItems);
       if (i >= total) break;
+      if (i >= products) {
+        i = __shfl_sync(0xffffffffu, next, 0);
+        continue;
+      }
       const Piece q = piece_of(i, n_units, strips1, strips2, units);
       const int e = units[q.unit].expert, nkb = q.down ? kb2 : kb1;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int nk = min(kStageKb, nkb - kb0);
-        ok = mbar_wait_warp(&empty[st.slot], st.phase ^ 1, abort);
+        ok = mbar_wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         uint8_t* dst = ring + st.slot * a.stage_bytes;
         uint64_t* bar = &full_w[st.slot];
@@ -380,6 +412,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
       if (lane == 0) mbar_arrive(&item_empty[it.slot]);
       it.next(kItems);
       if (i < 0) break;
+      if (i >= products) continue;
       const Piece q = piece_of(i, n_units, strips1, strips2, units);
       const FewUnit u = units[q.unit];
       const int n = __popcll(u.tokens), nkb = q.down ? kb2 : kb1, parts = q.down ? 2 : 1;
@@ -412,53 +445,91 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
       uint8_t* dst = ring + a.row_offset + (part * a.cap + j) * kPitch;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int bytes = min(kStageKb, nkb - kb0) * 128;
-        ok = mbar_wait_warp(&empty[st.slot], st.phase ^ 1, abort);
+        ok = mbar_wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         uint64_t* bar = &full_x[st.slot];
         if (lane == 0) mbar_arrive_expect_tx(bar, n * parts * bytes);
         __syncwarp();
-        if (src) bulk_load(dst + st.slot * a.stage_bytes, src + kb0 * 128, bytes, bar);
+        if (src) bulk_load(dst + st.slot * a.row_stage_bytes, src + kb0 * 128, bytes, bar);
         ++issued;
-        st.next(a.stages);
+        st.next(a.row_stages);
       }
     }
     if (!ok) {
       abort_s = 1;
       int never = 0;
-      for (int j = min(issued, a.stages); j > 0; --j) {
+      for (int j = min(issued, a.row_stages); j > 0; --j) {
         const int n = issued - j;
-        mbar_wait_warp(&full_x[n % a.stages], (n / a.stages) & 1, &never);
+        mbar_wait_warp(&full_x[n % a.row_stages], (n / a.row_stages) & 1, &never);
       }
     }
-  } else {
-    // ------------------------------------------------ products
-    const int group = warp >> 3, kb_own = warp & 7, g = lane >> 2, t = lane & 3;
-    Slot st, it;
-    int turn = 0;  // of the groups
-    float* reduce = reinterpret_cast<float*>(ring + a.reduce_offset);  // [warp][kRows][8]
-    for (;;) {
-      if (ok) ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
-      if (!ok) abort_s = 1;
-      // a wait that ran out in one warp ends all of them, here and together:
-      // they meet at barriers
-      uint32_t lost;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t"
-          "setp.ne.u32 p, %1, 0;\n\t"
-          "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
-          "selp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(lost)
-          : "r"(ok ? 0u : 1u), "n"(kThreads)
-          : "memory");
-      if (lost) {
-        ok = false;
-        break;
-      }
+  } else if (warp == kWarps + 2) {
+    // ------------------------------------------------ news of finished strips
+    Slot it;
+    while (ok) {
+      ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
+      if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
+      if (i >= 0 && i < products) {
+        ok = mbar_wait_warp(&item_done[it.slot], it.phase, abort);
+        if (!ok) break;
+        const Piece q = piece_of(i, n_units, strips1, strips2, units);
+        if (lane == 0) add_release(q.down ? p.strips + q.strip : p.ready + q.unit, 1);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[it.slot]);
       it.next(kItems);
       if (i < 0) break;
+    }
+    if (!ok) abort_s = 1;
+  } else {
+    // ------------------------------------------------ products
+    const int group = warp >> 3, kb_own = warp & 7, g = lane >> 2, t = lane & 3;
+    Slot st, row_st, it;
+    int turn = 0, buffer = 0;  // of the groups; of the sums
+    float* const reduce = reinterpret_cast<float*>(ring + a.reduce_offset);  // [2][8 warps][kRows][8]
+    for (;;) {
+      // A wait that ran out in one warp ends all of them, together: they meet
+      // at the next or-reduction, one for each piece of a product and one at
+      // the end, and none waits for a barrier that another does not reach.
+      if (ok) ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
+      if (!ok) {
+        abort_s = 1;
+        if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
+        any_of<kThreads>(true);
+        break;
+      }
+      const int slot = it.slot, i = *reinterpret_cast<volatile int32_t*>(&item[slot]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[slot]);
+      it.next(kItems);
+      if (i < 0) {
+        ok = !any_of<kThreads>(false);
+        break;
+      }
+      if (i >= products) {
+        // the gated sum of some columns of some tokens, once every unit has
+        // its part of them
+        const int col0 = (i - products) / sum_groups * kSumCols, t0 = (i - products) % sum_groups * kSumTokens;
+        const uint64_t begin = global_timer_ns();
+        for (int s = col0 / kRows; s * kRows < col0 + kSumCols; ++s)
+          while (ok && load_acquire(p.strips + s) != n_units)
+            if (*abort || global_timer_ns() - begin > kWaitLimitNs) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        for (int o = threadIdx.x; o < kSumCols * min(kSumTokens, p.T - t0); o += kThreads) {
+          const int token = t0 + o / kSumCols, n = col0 + o % kSumCols;
+          float s = 0.0f;
+#pragma unroll 8
+          for (int j = 0; j < p.k; ++j) {
+            const float w = __ldg(p.topk_w + token * p.k + j);
+            const int row = __ldg(p.pair_row + token * p.k + j);
+            s = fmaf(w, __ldcg(p.y + static_cast<int64_t>(row) * p.d + n), s);
+          }
+          static_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(token) * p.d + n] = __float2bfloat16_rn(s);
+        }
+        continue;
+      }
       const Piece q = piece_of(i, n_units, strips1, strips2, units);
       const FewUnit u = units[q.unit];
       const int n_tok = __popcll(u.tokens), nkb = q.down ? kb2 : kb1;
@@ -466,8 +537,8 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
       float acc[kTiles][2][4] = {};
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         if (turn == group) {
-          ok = mbar_wait_warp(&full_w[st.slot], st.phase, abort);
-          if (ok) ok = mbar_wait_warp(&full_x[st.slot], st.phase, abort);
+          ok = mbar_wait_warp(&full_x[row_st.slot], row_st.phase, abort);
+          if (ok) ok = mbar_wait_warp(&full_w[st.slot], st.phase, abort);
           if (!ok) {
             abort_s = 1;
             break;
@@ -489,7 +560,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
               scales = record + int4_scale_offset(p.group, kb_own & 1);
             }
             // columns without a token read the first one's row
-            const uint8_t* r0 = base + a.row_offset + kb_own * 128;
+            const uint8_t* r0 = ring + a.row_offset + row_st.slot * a.row_stage_bytes + kb_own * 128;
             const uint8_t* const rows[2] = {r0 + (g < n_tok ? g : 0) * kPitch, r0 + (8 + g < n_tok ? 8 + g : 0) * kPitch};
             const int low = q.down ? a.cap * kPitch : 0;
             if (two)
@@ -498,34 +569,52 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
               Multiply<kKind>::template block<false>(acc, w, scales, q.down, groups, rows, low, lane);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[st.slot]);
+          if (lane == 0) {
+            mbar_arrive(&empty_w[st.slot]);
+            mbar_arrive(&empty_x[row_st.slot]);
+          }
         }
         st.next(a.stages);
+        row_st.next(a.row_stages);
         if (++turn == F::kGroups) turn = 0;
       }
-      for (int n = 0; n < (two ? 2 : 1); ++n) {
+      bool lost = false;
+      for (int n = 0; n < (two ? 2 : 1) && !lost; ++n) {
+        // Eight partial sums of every value, the second group's added to the
+        // first's.  A buffer is written again after the next barrier but one
+        // at the earliest, when all have read it.
+        float* const sums = reduce + buffer * (8 * kRows * 8);
+        buffer ^= 1;
+        if (F::kGroups == 2 && group == 1) asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + kb_own) : "memory");
 #pragma unroll
         for (int m = 0; m < kTiles; ++m)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int row = kKind == MOE_WEIGHTS_BF16 ? half * (kRows / 2) + 8 * m + g : 16 * m + 8 * half + g;
-            const float2 v = n == 0 ? make_float2(acc[m][0][2 * half], acc[m][0][2 * half + 1])
-                                    : make_float2(acc[m][1][2 * half], acc[m][1][2 * half + 1]);
-            *reinterpret_cast<float2*>(reduce + (warp * kRows + row) * 8 + 2 * t) = v;
+            float2 v = n == 0 ? make_float2(acc[m][0][2 * half], acc[m][0][2 * half + 1])
+                              : make_float2(acc[m][1][2 * half], acc[m][1][2 * half + 1]);
+            auto* to = reinterpret_cast<float2*>(sums + (kb_own * kRows + row) * 8 + 2 * t);
+            if (F::kGroups == 2 && group == 1) {
+              v.x += to->x;
+              v.y += to->y;
+            }
+            *to = v;
           }
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
+        lost = any_of<kThreads>(!ok);
         constexpr float kLift = kKind == MOE_WEIGHTS_FP8 ? kFp8Lift : 1.0f;
         const int tok = 8 * n + (threadIdx.x & 7);
-        if (tok < n_tok) {
+        if (tok < n_tok && !lost) {
+          const float* own = sums + (threadIdx.x & 7);
           if (!q.down) {
             for (int feature = threadIdx.x >> 3; feature < kRows / 2; feature += kThreads / 8) {
               const int row = kKind == MOE_WEIGHTS_FP8 ? feature / 16 * 32 + feature % 16 : feature;
               constexpr int kToUp = kKind == MOE_WEIGHTS_FP8 ? 16 : kRows / 2;
               float gate = 0.0f, up = 0.0f;
 #pragma unroll
-              for (int v = 0; v < kWarps; ++v) {
-                gate += reduce[(v * kRows + row) * 8 + (threadIdx.x & 7)];
-                up += reduce[(v * kRows + row + kToUp) * 8 + (threadIdx.x & 7)];
+              for (int v = 0; v < 8; ++v) {
+                gate += own[(v * kRows + row) * 8];
+                up += own[(v * kRows + row + kToUp) * 8];
               }
               gate *= kLift;
               up *= kLift;
@@ -540,41 +629,19 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
             for (int row = threadIdx.x >> 3; row < kRows; row += kThreads / 8) {
               float y = 0.0f;
 #pragma unroll
-              for (int v = 0; v < kWarps; ++v) y += reduce[(v * kRows + row) * 8 + (threadIdx.x & 7)];
+              for (int v = 0; v < 8; ++v) y += own[(v * kRows + row) * 8];
               p.y[static_cast<int64_t>(u.row + tok) * p.d + q.strip * kRows + row] = y * kLift;
             }
           }
         }
-        if (!q.down) fence_proxy_global();  // h is read by bulk copies
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
       }
-      if (!q.down) {
-        if (threadIdx.x == 0) {
-          __threadfence();
-          add_release(p.ready + q.unit, 1);
-        }
-        continue;
+      if (lost) {
+        ok = false;
+        break;
       }
-      // the last unit of these output features adds them up for every token
-      if (threadIdx.x == 0) {
-        __threadfence();
-        last_s = atomicAdd(p.strips + q.strip, 1) == n_units - 1;
-        __threadfence();
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-      if (last_s) {
-        for (int o = threadIdx.x; o < p.T * kRows; o += kThreads) {
-          const int token = o / kRows, n = q.strip * kRows + o % kRows;
-          float s = 0.0f;
-#pragma unroll 8
-          for (int j = 0; j < p.k; ++j) {
-            const float w = __ldg(p.topk_w + token * p.k + j);
-            const int row = __ldg(p.pair_row + token * p.k + j);
-            s = fmaf(w, __ldcg(p.y + static_cast<int64_t>(row) * p.d + n), s);
-          }
-          static_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(token) * p.d + n] = __float2bfloat16_rn(s);
-        }
-      }
+      if (!q.down) fence_proxy_global();  // h is read by bulk copies
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_done[slot]);
     }
   }
   if (!ok && lane == 0) record_status(&p.header->status, kStatusTimeout);
@@ -583,17 +650,20 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 2) * 32, 1) few_
 template <int kKind>
 cudaError_t launch(Args& a, int weight_bytes, int scale_bytes, int num_sms, cudaStream_t stream) {
   using F = Format<kKind>;
-  constexpr int kReduce = F::kGroups * 8 * F::kRows * 8 * 4;
+  constexpr int kReduce = 2 * 8 * F::kRows * 8 * 4;
   a.scale_offset = weight_bytes;
-  a.row_offset = weight_bytes + scale_bytes;
-  a.stage_bytes = static_cast<int>(align_up(a.row_offset + 2 * a.cap * (kStageKb * 128 + F::kPad), 128));
-  a.stages = static_cast<int>((kSmemMost - kReduce) / a.stage_bytes);
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  a.reduce_offset = a.stages * a.stage_bytes;
+  a.stage_bytes = static_cast<int>(align_up(weight_bytes + scale_bytes, 128));
+  a.row_stage_bytes = static_cast<int>(align_up(2 * a.cap * (kStageKb * 128 + F::kPad), 128));
+  // rows come from the L2 and need fewer stages in flight than weights do
+  a.row_stages = a.cap <= 4 ? 4 : a.cap <= 8 ? 3 : 2;
+  const int rest = static_cast<int>(kSmemMost) - kReduce - a.row_stages * a.row_stage_bytes;
+  a.stages = rest / a.stage_bytes < kMaxStages ? rest / a.stage_bytes : kMaxStages;
+  a.row_offset = a.stages * a.stage_bytes;
+  a.reduce_offset = a.row_offset + a.row_stages * a.row_stage_bytes;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t err = allow(reinterpret_cast<const void*>(few_experts_kernel<kKind>), allowed, kSmemMost, false);
   if (err != cudaSuccess) return err;
-  return launch_dependent(few_experts_kernel<kKind>, dim3(num_sms), dim3((F::kGroups * 8 + 2) * 32),
+  return launch_dependent(few_experts_kernel<kKind>, dim3(num_sms), dim3((F::kGroups * 8 + 3) * 32),
                           a.reduce_offset + kReduce, stream, a);
 }
 

@@ -30,7 +30,7 @@ def run(kind, T, d, E, k, f, group=128, renormalize=True, logits=None, seed=0, *
     assert torch.equal(idx_out.long(), idx)
     assert float((w_out - w).abs().max()) <= 2.0 ** -20
     want, bound = ref.layer(x, idx, w, mats, kind)
-    ref.check(out, want, bound, kind)
+    ref.check(out, want, bound)
     return out
 
 
@@ -110,7 +110,7 @@ def test_infinite_weights_of_experts_not_chosen():
     keep = [t for t in range(T) if t != 6]
     idx, w = ref.route(logits[keep], 2)
     want, bound = ref.layer(x[keep], idx, w, mats, "bf16")
-    ref.check(out[keep], want, bound, "bf16")
+    ref.check(out[keep], want, bound)
     assert torch.isnan(out[6]).all()
 
 
@@ -134,7 +134,7 @@ def test_routed(kind, T, d, E, k, f):
     idx, w = ref.route(logits, k)
     assert torch.equal(idx_out.long(), idx)
     want, bound = ref.layer(x, idx, w, mats, kind, d_logit)
-    ref.check(out, want, bound, kind)
+    ref.check(out, want, bound)
 
 
 def test_same_bits_every_time_whatever_the_workspace_held():
@@ -230,10 +230,10 @@ def test_captured_graphs_that_share_a_workspace(kind):
             g.replay()
         torch.cuda.synchronize()
         idx, w = ref.route(l1, k)
-        ref.check(o1, *ref.layer(x1, idx, w, mats, kind), kind)
+        ref.check(o1, *ref.layer(x1, idx, w, mats, kind))
         logits = x2.double() @ router_w.double()
         idx, w = ref.route(logits, k)
-        ref.check(o2, *ref.layer(x2, idx, w, mats, kind, 1e-4), kind)
+        ref.check(o2, *ref.layer(x2, idx, w, mats, kind, 1e-4))
 
 
 def test_argument_checks():

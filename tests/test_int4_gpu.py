@@ -24,9 +24,9 @@ def check_linear(x, codes, scales, group, out):
     # a code may be multiplied as 16 + code (below 32) with 24 times the inputs' sum taken off again: 56 scales a product
     bound = ref.U * want.abs() + ref.gamma(K) * 7.0 * (x.double().abs() @ (8.0 * scales.double().abs().repeat_interleave(
         group, 0)[:K])) + 2.0 ** -120
-    err = (out.double() - want).abs()
-    assert float((err / bound).max()) <= 1.0
-    assert float(err.norm() / want.norm()) <= 1.25 * ref.U / 3.0 ** 0.5
+    # (the whole is then within U too; less, U / sqrt(3), is what roundings come to on average, and a few values that
+    # make up most of the norm need not keep to the average)
+    ref.check(out, want, bound)
 
 
 @pytest.mark.parametrize("M", list(range(1, 17)))
