@@ -26,10 +26,12 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p) {  // of input 
 
 // acc[tile][n][..] += tile's 16 rows x 8 columns n.  w: the codes of the 64
 // inputs; groups: scales that they have, 1 or 2; rows[n]: the values of this
-// lane's column, 128 bytes; low: bytes to their low parts, or 0.
+// lane's column, 128 bytes; low: bytes to their low parts, or 0; chunks: how
+// many of the row's eight 16-byte chunks there are (the others count as zeros).
 template <bool kTwo>
 __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t* w, const uint8_t* scales, int groups,
-                                           const uint8_t* const (&rows)[2], int low, int lane) {
+                                           const uint8_t* const (&rows)[2], int low, int lane,
+                                           int chunks = 8) {
   constexpr int kN = kTwo ? 2 : 1;
   constexpr uint32_t kMinus = 0xbfc0bfc0u;  // -1.5
   const int g = lane >> 2, t = lane & 3;
@@ -39,7 +41,7 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      b[c][n] = *reinterpret_cast<const uint4*>(rows[n] + c * 64 + t * 16);
+      b[c][n] = 4 * c + t < chunks ? *reinterpret_cast<const uint4*>(rows[n] + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) start[c][n][i] = c == 1 && groups == 1 ? start[0][n][i] : 0.0f;
       mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, b[c][n].x, b[c][n].y);
