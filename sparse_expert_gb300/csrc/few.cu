@@ -47,10 +47,12 @@ constexpr int kUnitCache = 512;                  // units kept in shared memory
 constexpr size_t kSmemMost = 227 * 1024 - 1024 - sizeof(FewUnit) * kUnitCache;  // less the static variables
 
 // Rows of a strip, groups of eight multiplying warps (a group takes every
-// kGroups-th stage: decoding codes takes more issue slots than one group has),
-// and the padding of a token's row, with which the eight lanes that a 16-byte
+// kGroups-th stage), and the padding of a token's row, with which the eight lanes that a 16-byte
 // shared load serves at once meet different banks: two rows of 64 bytes 64
 // apart, or, where a lane reads 32 bytes, 16 apart.
+// Groups, one or two, as measured (us): bf16 1T layer, 4 tokens, 388 and 408;
+// FP8 1T layer, 32 tokens, 1,717 and 1,550; 4 bits 7B-A1B layer, 48 tokens, 152
+// and 207 (two groups leave 96 registers a thread, and that kernel spills).
 template <int kKind>
 struct Format;
 template <>
@@ -63,7 +65,7 @@ struct Format<MOE_WEIGHTS_FP8> {
 };
 template <>
 struct Format<MOE_WEIGHTS_INT4> {
-  static constexpr int kRows = 64, kGroups = 2, kPad = 64;
+  static constexpr int kRows = 64, kGroups = 1, kPad = 64;
 };
 
 struct Args {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
     for (int i = first_s;;) {
       int next = 0;
       if (lane == 0) next = atomicAdd(&p.header->ticket, 1);
-      ok = mbar_wait_warp(&item_empty[it.slot], it.phase ^ 1, abort);
+      ok = wait_warp(&item_empty[it.slot], it.phase ^ 1, abort);
       if (!ok) break;
       if (lane == 0) {
         item[it.slot] = i < total ? i : -1;
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       const int e = units[q.unit].expert, nkb = q.down ? kb2 : kb1;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int nk = min(kStageKb, nkb - kb0);
-        ok = mbar_wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         uint8_t* dst = ring + st.slot * a.stage_bytes;
         uint64_t* bar = &full_w[st.slot];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       int never = 0;
       for (int j = min(issued, a.stages); j > 0; --j) {
         const int n = issued - j;
-        mbar_wait_warp(&full_w[n % a.stages], (n / a.stages) & 1, &never);
+        wait_warp(&full_w[n % a.stages], (n / a.stages) & 1, &never);
       }
     }
   } else if (warp == kWarps + 1) {
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
     Slot st, it;
     int issued = 0, complete = -1;
     while (ok) {
-      ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
+      ok = wait_warp(&item_full[it.slot], it.phase, abort);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       __syncwarp();
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       uint8_t* dst = ring + a.row_offset + (part * a.cap + j) * kPitch;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int bytes = min(kStageKb, nkb - kb0) * 128;
-        ok = mbar_wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         uint64_t* bar = &full_x[st.slot];
         if (lane == 0) mbar_arrive_expect_tx(bar, n * parts * bytes);
@@ -460,18 +462,18 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       int never = 0;
       for (int j = min(issued, a.row_stages); j > 0; --j) {
         const int n = issued - j;
-        mbar_wait_warp(&full_x[n % a.row_stages], (n / a.row_stages) & 1, &never);
+        wait_warp(&full_x[n % a.row_stages], (n / a.row_stages) & 1, &never);
       }
     }
   } else if (warp == kWarps + 2) {
     // ------------------------------------------------ news of finished strips
     Slot it;
     while (ok) {
-      ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
+      ok = wait_warp(&item_full[it.slot], it.phase, abort);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       if (i >= 0 && i < products) {
-        ok = mbar_wait_warp(&item_done[it.slot], it.phase, abort);
+        ok = wait_warp(&item_done[it.slot], it.phase, abort);
         if (!ok) break;
         const Piece q = piece_of(i, n_units, strips1, strips2, units);
         if (lane == 0) add_release(q.down ? p.strips + q.strip : p.ready + q.unit, 1);
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       // A wait that ran out in one warp ends all of them, together: they meet
       // at the next or-reduction, one for each piece of a product and one at
       // the end, and none waits for a barrier that another does not reach.
-      if (ok) ok = mbar_wait_warp(&item_full[it.slot], it.phase, abort);
+      if (ok) ok = wait_warp(&item_full[it.slot], it.phase, abort);
       if (!ok) {
         abort_s = 1;
         if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
@@ -537,8 +539,8 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       float acc[kTiles][2][4] = {};
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         if (turn == group) {
-          ok = mbar_wait_warp(&full_x[row_st.slot], row_st.phase, abort);
-          if (ok) ok = mbar_wait_warp(&full_w[st.slot], st.phase, abort);
+          ok = wait_warp(&full_x[row_st.slot], row_st.phase, abort);
+          if (ok) ok = wait_warp(&full_w[st.slot], st.phase, abort);
           if (!ok) {
             abort_s = 1;
             break;

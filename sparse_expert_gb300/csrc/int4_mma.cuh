@@ -43,7 +43,7 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
     for (int n = 0; n < kN; ++n) {
       b[c][n] = 4 * c + t < chunks ? *reinterpret_cast<const uint4*>(rows[n] + c * 64 + t * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) start[c][n][i] = c == 1 && groups == 1 ? start[0][n][i] : 0.0f;
+      for (int i = 0; i < 4; ++i) start[c][n][i] = 0.0f;
       mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, b[c][n].x, b[c][n].y);
       mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, b[c][n].z, b[c][n].w);
       if (low) {
@@ -52,6 +52,12 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
         mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, l.z, l.w);
       }
     }
+  if (groups == 1) {  // one group: both halves' start
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) start[0][n][i] += start[1][n][i];
+  }
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
     const uint4 code = *reinterpret_cast<const uint4*>(w + (m * 32 + lane) * 16);
@@ -60,14 +66,6 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint32_t top = c ? code.y : code.x, bottom = c ? code.w : code.z;
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c == 0)
-            sum[n][i] = groups == 1 ? start[1][n][i] : start[0][n][i];
-          else if (groups == 2)
-            sum[n][i] = start[1][n][i];
       uint32_t v[4][2];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
@@ -76,7 +74,10 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        mma_bf16(sum[n], v[0][0], v[0][1], v[1][0], v[1][1], b[c][n].x, b[c][n].y);
+        if (c == 0 || groups == 2)
+          mma_bf16_from(sum[n], start[c][n], v[0][0], v[0][1], v[1][0], v[1][1], b[c][n].x, b[c][n].y);
+        else
+          mma_bf16(sum[n], v[0][0], v[0][1], v[1][0], v[1][1], b[c][n].x, b[c][n].y);
         mma_bf16(sum[n], v[2][0], v[2][1], v[3][0], v[3][1], b[c][n].z, b[c][n].w);
         if (low) {
           const uint4 l = *reinterpret_cast<const uint4*>(rows[n] + low + c * 64 + t * 16);

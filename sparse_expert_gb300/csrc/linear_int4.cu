@@ -78,7 +78,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
     int issued = 0;
     for (int strip = first; strip < a.strips && ok; strip += step)
       for (int u = unit0; u < unit1; u += kStageUnits) {
-        ok = mbar_wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         if (lane == 0) {
           const int bytes = min(kStageUnits, unit1 - u) * record;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
       abort_s = 1;
       int never = 0;
       for (int j = min(issued, kStages); j > 0; --j)
-        mbar_wait_warp(&full_w[(issued - j) % kStages], ((issued - j) / kStages) & 1, &never);
+        wait_warp(&full_w[(issued - j) % kStages], ((issued - j) / kStages) & 1, &never);
     }
   } else if (warp == kWarps + 1) {
     Slot st;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
     const uint8_t* src = lane < p.M ? static_cast<const uint8_t*>(p.x) + lane * p.x_stride * 2 : nullptr;
     for (int strip = first; strip < a.strips && ok; strip += step)
       for (int u = unit0; u < unit1; u += kStageUnits) {
-        ok = mbar_wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
         if (!ok) break;
         const int k0 = u * kInt4Unit, bytes = 2 * (min(p.K, min(unit1, u + kStageUnits) * kInt4Unit) - k0);
         if (lane == 0) mbar_arrive_expect_tx(&full_x[st.slot], p.M * bytes);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
       abort_s = 1;
       int never = 0;
       for (int j = min(issued, kRowStages); j > 0; --j)
-        mbar_wait_warp(&full_x[(issued - j) % kRowStages], ((issued - j) / kRowStages) & 1, &never);
+        wait_warp(&full_x[(issued - j) % kRowStages], ((issued - j) / kRowStages) & 1, &never);
     }
   } else {
     const int g = lane >> 2, t = lane & 3;
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
     for (int strip = first; strip < a.strips; strip += step) {
       float acc[4][2][4] = {};
       for (int u = unit0; u < unit1 && ok; u += kStageUnits) {
-        ok = mbar_wait_warp(&full_x[row_st.slot], row_st.phase, abort);
-        if (ok) ok = mbar_wait_warp(&full_w[st.slot], st.phase, abort);
+        ok = wait_warp(&full_x[row_st.slot], row_st.phase, abort);
+        if (ok) ok = wait_warp(&full_w[st.slot], st.phase, abort);
         if (!ok) {
           abort_s = 1;
           break;
