@@ -51,8 +51,8 @@ constexpr size_t kSmemMost = 227 * 1024 - 1024 - sizeof(FewUnit) * kUnitCache;  
 // shared load serves at once meet different banks: two rows of 64 bytes 64
 // apart, or, where a lane reads 32 bytes, 16 apart.
 // Groups, one or two, as measured (us): bf16 1T layer, 4 tokens, 388 and 408;
-// FP8 1T layer, 32 tokens, 1,717 and 1,550; 4 bits 7B-A1B layer, 48 tokens, 152
-// and 207 (two groups leave 96 registers a thread, and that kernel spills).
+// FP8 1T layer, 32 tokens, 1,717 and 1,550; 4 bits 7B-A1B layer, 48 tokens, 144
+// and 200 (two groups leave 96 registers a thread, and that kernel spills).
 template <int kKind>
 struct Format;
 template <>

@@ -28,10 +28,10 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p) {  // of input 
 // inputs; groups: scales that they have, 1 or 2; rows[n]: the values of this
 // lane's column, 128 bytes; low: bytes to their low parts, or 0; chunks: how
 // many of the row's eight 16-byte chunks there are (the others count as zeros).
-template <bool kTwo>
-__device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t* w, const uint8_t* scales, int groups,
-                                           const uint8_t* const (&rows)[2], int low, int lane,
-                                           int chunks = 8) {
+template <bool kTwo, bool kLow, int kGroups>
+__device__ __forceinline__ void int4_block_of(float (&acc)[4][2][4], const uint8_t* w, const uint8_t* scales,
+                                              const uint8_t* const (&rows)[2], int low, int lane, int chunks, int any_groups = 0) {
+  const int groups = kGroups ? kGroups : any_groups;
   constexpr int kN = kTwo ? 2 : 1;
   constexpr uint32_t kMinus = 0xbfc0bfc0u;  // -1.5
   const int g = lane >> 2, t = lane & 3;
@@ -46,7 +46,7 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
       for (int i = 0; i < 4; ++i) start[c][n][i] = 0.0f;
       mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, b[c][n].x, b[c][n].y);
       mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, b[c][n].z, b[c][n].w);
-      if (low) {
+      if (kLow) {
         const uint4 l = *reinterpret_cast<const uint4*>(rows[n] + low + c * 64 + t * 16);
         mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, l.x, l.y);
         mma_bf16(start[c][n], kMinus, kMinus, kMinus, kMinus, l.z, l.w);
@@ -79,7 +79,7 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
         else
           mma_bf16(sum[n], v[0][0], v[0][1], v[1][0], v[1][1], b[c][n].x, b[c][n].y);
         mma_bf16(sum[n], v[2][0], v[2][1], v[3][0], v[3][1], b[c][n].z, b[c][n].w);
-        if (low) {
+        if (kLow) {
           const uint4 l = *reinterpret_cast<const uint4*>(rows[n] + low + c * 64 + t * 16);
           mma_bf16(sum[n], v[0][0], v[0][1], v[1][0], v[1][1], l.x, l.y);
           mma_bf16(sum[n], v[2][0], v[2][1], v[3][0], v[3][1], l.z, l.w);
@@ -94,6 +94,26 @@ __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t*
           for (int i = 0; i < 4; ++i) acc[m][n][i] = fmaf(i < 2 ? s0 : s1, sum[n][i], acc[m][n][i]);
       }
     }
+  }
+}
+
+// The same by how many scales and parts there are, which no block changes: the
+// forms have no tests inside (48 tokens of the 7B-A1B layer: 144 us, 152 with
+// them; moe_linear_int4's kernel has fewer registers and is better off with
+// one form, 162 us where forms give 170).
+template <bool kTwo>
+__device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t* w, const uint8_t* scales, int groups,
+                                           const uint8_t* const (&rows)[2], int low, int lane, int chunks = 8) {
+  if (low) {
+    if (groups == 2)
+      int4_block_of<kTwo, true, 2>(acc, w, scales, rows, low, lane, chunks);
+    else
+      int4_block_of<kTwo, true, 1>(acc, w, scales, rows, low, lane, chunks);
+  } else {
+    if (groups == 2)
+      int4_block_of<kTwo, false, 2>(acc, w, scales, rows, low, lane, chunks);
+    else
+      int4_block_of<kTwo, false, 1>(acc, w, scales, rows, low, lane, chunks);
   }
 }
 

@@ -142,9 +142,9 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
           const uint8_t* scales = r + int4_scale_offset(p.group, warp & 1);
           const int groups = p.group == 32 ? 2 : 1, chunks = left / 8;
           if (two)
-            int4_block<true>(acc, codes, scales, groups, rows, 0, lane, chunks);
+            int4_block_of<true, false, 0>(acc, codes, scales, rows, 0, lane, chunks, groups);
           else
-            int4_block<false>(acc, codes, scales, groups, rows, 0, lane, chunks);
+            int4_block_of<false, false, 0>(acc, codes, scales, rows, 0, lane, chunks, groups);
         }
         __syncwarp();
         if (lane == 0) {
