@@ -622,10 +622,14 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
               up *= kLift;
               const float h = gate / (1.0f + __expf(-gate)) * up;
               const int64_t at = static_cast<int64_t>(u.row + tok) * p.f + q.strip * (kRows / 2) + feature;
-              const __nv_bfloat16 high = __float2bfloat16_rn(h);
+              // Rounded to nearest, the largest finite values would become
+              // infinite: their high part is cut off instead.  An infinity has
+              // no remainder (its difference from itself would be NaN).
+              __nv_bfloat16 high = __float2bfloat16_rn(h);
+              if (isinf(__bfloat162float(high))) high = __float2bfloat16_rz(h);
               auto* to = static_cast<__nv_bfloat16*>(p.h);
               to[at] = high;
-              to[a.low_offset / 2 + at] = __float2bfloat16_rn(h - __bfloat162float(high));
+              to[a.low_offset / 2 + at] = __float2bfloat16_rn(isinf(h) ? 0.0f : h - __bfloat162float(high));
             }
           } else {
             for (int row = threadIdx.x >> 3; row < kRows; row += kThreads / 8) {

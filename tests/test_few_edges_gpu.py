@@ -1,0 +1,37 @@
+"""The layer for a few tokens and 4-bit products where values, codes, groups and sizes are at their ends."""
+import math
+
+import pytest
+import torch
+
+from tests import few_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("sparse_expert_gb300")
+
+KINDS = ["bf16", "fp8", "int4"]
+
+
+def bf16(*shape, value):
+    return torch.full(shape, value, dtype=torch.bfloat16, device="cuda")
+
+
+def test_h_up_to_the_largest_fp32_value_and_infinity():
+    """h = x^2 (129 * 254 / 2^13) of rows whose x is one power of two: 2^127 * 1.99988, which a bf16 alone would round
+    to infinity, is kept; beyond fp32 h is an infinity, and so is out, not NaN."""
+    d = f = 64
+    # 64 equal products: the sums are exact
+    gate, up = bf16(1, d, f, value=2.0 ** -6 * 129 / 128), bf16(1, d, f, value=2.0 ** -5 * 254 / 128)
+    down = bf16(1, f, d, value=2.0 ** -40)
+    down[..., ::2] *= -1.0
+    packed = moe.moe_pack_weights(gate, up, down)
+    x = torch.tensor([64.0, 2.0 ** 63, 2.0 ** 65, -(2.0 ** 62)], device="cuda")[:, None].repeat(1, d).to(torch.bfloat16)
+    out = moe.moe_forward_few(x, torch.zeros(4, 1, device="cuda"), packed, 1, 1, f)
+    sign = torch.where(torch.arange(d, device="cuda") % 2 == 0, -1.0, 1.0).double()
+    for row, v in ((0, 64.0), (1, 2.0 ** 63)):
+        # h is good to U^2 and the gate's 2^-20, out to U
+        want = v * v * (129 * 254 / 2 ** 13) * 2.0 ** -34 * sign
+        assert float(((out[row].double() - want) / want).abs().max()) <= ref.U + ref.U ** 2 + 2.0 ** -20 + ref.gamma(64)
+    assert torch.equal(out[2].double(), math.inf * sign)
+    assert (out[3] == 0).all()  # silu of a large negative number
