@@ -1,12 +1,15 @@
 // Products of 64 inner indices of a strip of 4-bit weights (int4.cuh) with up
 // to 16 rows of bf16 values, on the tensor cores.
 //
-// A code q becomes the bf16 value 1 + q / 16 by one AND-OR of its bits under
-// the exponent of one.  (q - 8) / 16 = that - 1.5, so the sums of a group of
-// inputs start at -1.5 times the sum of its inputs, which the tensor cores form
+// A code q becomes the bf16 value 4 + q / 4 by one AND-OR of its bits under
+// the exponent of four.  (q - 8) / 4 = that - 6, so the sums of a group of
+// inputs start at -6 times the sum of its inputs, which the tensor cores form
 // with a constant operand for all weight rows at once; then the group's sum
-// times 16 x scale, in fp32, goes to the strip's.  Codes are so multiplied
-// exactly, and what cancels is at most 7 times the largest weight's share.
+// times 4 x scale, in fp32, goes to the strip's.  Codes are so multiplied
+// exactly, and what cancels is at most 7 times the largest weight's share.  (Any
+// power of two would do: with four, neither 4 x the largest scale that a
+// quantiser can make of bf16 weights, 2^125.2, nor the sums of inputs below
+// 2^118 leave the range of fp32.  An infinite input makes the sums NaN.)
 #pragma once
 
 #include "few.cuh"
@@ -21,7 +24,7 @@ __device__ __forceinline__ int int4_scale_offset(int group, int second) {
 
 __device__ __forceinline__ uint32_t int4_pair(uint32_t w, int p) {  // of input 2p and 2p + 1
   const uint32_t v = p == 0 ? w << 3 : w >> (4 * p - 3);
-  return (v & 0x00780078u) | 0x3f803f80u;
+  return (v & 0x00780078u) | 0x40804080u;
 }
 
 // acc[tile][n][..] += tile's 16 rows x 8 columns n.  w: the codes of the 64
@@ -33,7 +36,7 @@ __device__ __forceinline__ void int4_block_of(float (&acc)[4][2][4], const uint8
                                               const uint8_t* const (&rows)[2], int low, int lane, int chunks, int any_groups = 0) {
   const int groups = kGroups ? kGroups : any_groups;
   constexpr int kN = kTwo ? 2 : 1;
-  constexpr uint32_t kMinus = 0xbfc0bfc0u;  // -1.5
+  constexpr uint32_t kMinus = 0xc0c0c0c0u;  // -6
   const int g = lane >> 2, t = lane & 3;
   uint4 b[2][kN];
   float start[2][kN][4];  // of inputs 0 .. 31 and 32 .. 63
@@ -87,7 +90,7 @@ __device__ __forceinline__ void int4_block_of(float (&acc)[4][2][4], const uint8
       }
       if (c == 1 || groups == 2) {
         const int at = groups == 2 ? c * kInt4Rows : 0;
-        const float s0 = 16.0f * __bfloat162float(s[at]), s1 = 16.0f * __bfloat162float(s[at + 8]);
+        const float s0 = 4.0f * __bfloat162float(s[at]), s1 = 4.0f * __bfloat162float(s[at + 8]);
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll

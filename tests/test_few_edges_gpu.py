@@ -35,3 +35,19 @@ def test_h_up_to_the_largest_fp32_value_and_infinity():
         assert float(((out[row].double() - want) / want).abs().max()) <= ref.U + ref.U ** 2 + 2.0 ** -20 + ref.gamma(64)
     assert torch.equal(out[2].double(), math.inf * sign)
     assert (out[3] == 0).all()  # silu of a large negative number
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_scales_up_to_the_quantisers_largest(group):
+    """Weights near bf16's largest value: their scales are near 2^125."""
+    K, N = 256, 70
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    w = (torch.rand(K, N, generator=gen, device="cuda") * 2 - 1).mul_(2.0 ** 127 * 1.98).to(torch.bfloat16)
+    w[0::group] = 2.0 ** 127 * 1.984375  # of every group: the scale is 2^127 * 1.984375 / 7
+    codes, scales = moe.moe_quantize_int4(w, group)
+    assert float(scales.float().max()) >= 2.0 ** 125
+    x = (torch.randn(3, K, generator=gen, device="cuda") * 2.0 ** -20).to(torch.bfloat16)
+    out = moe.moe_linear_int4(x, moe.moe_pack_linear_int4(codes, scales, K, N, group), N, group)
+    dense = ref.dequantize_int4(codes, scales, group)
+    want, size = x.double() @ dense, x.double().abs() @ (8.0 * scales.double().repeat_interleave(group, 0))
+    ref.check(out, want, ref.U * want.abs() + 7.0 * ref.gamma(K) * size)
