@@ -492,7 +492,10 @@ MOE_API moe_status_t moe_forward_routed(const void* x, const void* router_packed
  *     MOE_WEIGHTS_INT4  moe_pack_weights_int4's with the same `group` (d and f
  *                       multiples of 128).  The weight is (code - 8) x scale;
  *                       codes are multiplied exactly, scales enter in fp32.
- *   group    of 4-bit weights; not looked at for the others.
+ *   group    of 4-bit weights, the one that they were packed with (packed
+ *            weights do not say it: with another one they are read as other
+ *            weights, up to 9 % beyond the end of a shorter buffer); not looked at
+ *            for the others.
  * h = silu(gate) * up is rounded to bf16, as everywhere in the layer; sums,
  * gates and the experts' outputs stay fp32 until out is rounded.  Results are
  * the same bits every time.  Logits must be finite (an expert with a logit of
@@ -533,7 +536,7 @@ MOE_API moe_status_t moe_forward_few_routed(const void* x, const void* router_pa
  *   256-byte aligned.
  * moe_pack_linear_int4, moe_linear_int4: one matrix, packed once into
  *   moe_linear_int4_packed_bytes(K, N, group) bytes (256-byte aligned), and
- *   its product with a few rows:
+ *   its product with a few rows, with the group that it was packed with:
  *     out[m, :] = bf16(x[m, :] @ w),  0 <= M <= MOE_LINEAR_INT4_MAX_ROWS,
  *   x [M, K] bf16 with x_stride values between rows (rows 16-byte aligned),
  *   out [M, N] bf16 with out_stride.  Codes are multiplied exactly, sums and

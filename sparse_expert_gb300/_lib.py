@@ -1148,6 +1148,15 @@ def _bytes_at_least(t, index, size, name):
     return t.data_ptr()
 
 
+def _packed_int4(t, index, size, group):
+    """A buffer of packed 4-bit weights.  It does not say what it was packed with, but its size does: another group
+    gives another size for the same matrices, and would be read as wrong weights.  (size 0: refused by the library.)"""
+    ptr = _bytes_at_least(t, index, size, "packed")
+    if size and t.numel() != size:
+        raise ValueError(f"packed has {t.numel()} bytes, weights of these sizes packed with group={group} have {size}")
+    return ptr
+
+
 def _forward_few(entry, where, x, route, route_ptr, packed, E, k, f, weights, group, renormalize, workspace, out,
                  topk_idx, topk_w, index):
     if x.dtype is not torch.bfloat16 or not x.is_contiguous():
@@ -1159,7 +1168,8 @@ def _forward_few(entry, where, x, route, route_ptr, packed, E, k, f, weights, gr
     kind = _WEIGHTS.get(weights)
     if kind is None:
         raise ValueError(f"weights must be one of {sorted(_WEIGHTS)}, got {weights!r}")
-    p_ptr = _bytes_at_least(packed, index, _packed_bytes(weights, E, d, f, group), "packed")
+    size = _packed_bytes(weights, E, d, f, group)
+    p_ptr = _packed_int4(packed, index, size, group) if kind == 2 else _bytes_at_least(packed, index, size, "packed")
     dev = x.device
     if workspace is None:
         size = moe_forward_few_workspace_bytes(T, E, k, d, f)
@@ -1181,8 +1191,8 @@ def moe_forward_few(x, logits, packed, E, k, f, weights="bf16", group=128, renor
                     topk_idx=None, topk_w=None, stream=None):
     """out [T,d] of the whole layer for T <= 64 tokens, routed by logits [T,E].
     weights: "bf16" (packed by moe_pack_weights), "fp8" (moe_pack_weights_fp8) or
-    "int4" (moe_pack_weights_int4, with the same group); topk_idx, topk_w
-    [T,k]: written where given."""
+    "int4" (moe_pack_weights_int4, with the same group: a buffer of another size
+    is refused); topk_idx, topk_w [T,k]: written where given."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_forward_few(x, logits, packed, E, k, f, weights, group, renormalize, workspace, out, topk_idx,
@@ -1282,8 +1292,8 @@ def moe_pack_linear_int4(codes, scales, K, N, group=128, stream=None):
 
 
 def moe_linear_int4(x, packed, N, group=128, out=None, stream=None):
-    """out [M,N] bf16 = x [M,K] bf16 (rows 16-byte aligned, any stride) times a matrix packed by moe_pack_linear_int4,
-    M <= 16.  out: [M,N] with unit stride along N, any row stride."""
+    """out [M,N] bf16 = x [M,K] bf16 (rows 16-byte aligned, any stride) times a matrix packed by moe_pack_linear_int4
+    with the same group (a buffer of another size is refused), M <= 16.  out: [M,N] with unit stride along N, any row stride."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_linear_int4(x, packed, N, group, out)
@@ -1294,7 +1304,7 @@ def moe_linear_int4(x, packed, N, group=128, out=None, stream=None):
         out, out_stride = torch.empty((M, N), dtype=torch.bfloat16, device=x.device), N
     else:
         out_stride = _rows(out, "out", index, (M, N), torch.bfloat16)
-    p_ptr = _bytes_at_least(packed, index, _linear_int4_bytes(K, N, group), "packed")
+    p_ptr = _packed_int4(packed, index, _linear_int4_bytes(K, N, group), group)
     status = lib.moe_linear_int4(x.data_ptr(), x_stride, p_ptr, M, K, N, group, out.data_ptr(), out_stride,
                                  _raw_stream(index))
     if status:

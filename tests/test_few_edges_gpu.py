@@ -51,3 +51,22 @@ def test_int4_scales_up_to_the_quantisers_largest(group):
     dense = ref.dequantize_int4(codes, scales, group)
     want, size = x.double() @ dense, x.double().abs() @ (8.0 * scales.double().repeat_interleave(group, 0))
     ref.check(out, want, ref.U * want.abs() + 7.0 * ref.gamma(K) * size)
+
+
+@pytest.mark.parametrize("packed_with,called_with", [(32, 64), (32, 128), (64, 128), (64, 32), (128, 64), (128, 32)])
+def test_weights_of_another_group_are_refused(packed_with, called_with):
+    """A buffer that was packed with other groups has another size."""
+    K, N, E = 256, 96, 3
+    codes, scales = moe.moe_quantize_int4(torch.randn(K, N, device="cuda").to(torch.bfloat16), packed_with)
+    x = torch.randn(2, K, device="cuda").to(torch.bfloat16)
+    matrix = moe.moe_pack_linear_int4(codes, scales, K, N, packed_with)
+    moe.moe_linear_int4(x, matrix, N, packed_with)
+    with pytest.raises(ValueError):
+        moe.moe_linear_int4(x, matrix, N, called_with)
+    experts, _ = ref.weights("int4", E, K, 128, packed_with)
+    logits = torch.randn(2, E, device="cuda")
+    moe.moe_forward_few(x, logits, experts, E, 2, 128, weights="int4", group=packed_with)
+    router = moe.moe_pack_router_weights(torch.randn(K, E, device="cuda").to(torch.bfloat16))
+    for call, route in ((moe.moe_forward_few, logits), (moe.moe_forward_few_routed, router)):
+        with pytest.raises(ValueError):
+            call(x, route, experts, E, 2, 128, weights="int4", group=called_with)
