@@ -524,8 +524,10 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
           float s = 0.0f;
 #pragma unroll 8
           for (int j = 0; j < p.k; ++j) {
-            const float w = __ldg(p.topk_w + token * p.k + j);
-            const int row = __ldg(p.pair_row + token * p.k + j);
+            // written by the previous launch while this one's blocks are
+            // already there: not for the read-only path
+            const float w = __ldcg(p.topk_w + token * p.k + j);
+            const int row = __ldcg(p.pair_row + token * p.k + j);
             s = fmaf(w, __ldcg(p.y + static_cast<int64_t>(row) * p.d + n), s);
           }
           static_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(token) * p.d + n] = __float2bfloat16_rn(s);

@@ -70,3 +70,19 @@ def test_weights_of_another_group_are_refused(packed_with, called_with):
     for call, route in ((moe.moe_forward_few, logits), (moe.moe_forward_few_routed, router)):
         with pytest.raises(ValueError):
             call(x, route, experts, E, 2, 128, weights="int4", group=called_with)
+
+
+def test_gates_that_change_from_call_to_call():
+    """Calls one after the other on one workspace, whose gates and choices differ: each uses its own."""
+    E, d, f, T, k = 6, 128, 128, 9, 3
+    packed, _ = ref.weights("bf16", E, d, f)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    routes = [torch.randn(T, E, generator=gen, device="cuda") * s for s in (0.1, 3.0, 1.0, 10.0)]
+    want = [moe.moe_forward_few(x, l, packed, E, k, f) for l in routes]
+    torch.cuda.synchronize()
+    ws = torch.empty(moe.moe_forward_few_workspace_bytes(T, E, k, d, f), dtype=torch.uint8, device="cuda")
+    idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    got = [moe.moe_forward_few(x, routes[i % 4], packed, E, k, f, workspace=ws, topk_idx=idx, topk_w=w) for i in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
