@@ -99,17 +99,31 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uin
   low = pack_bf16x2(a - low_f32(high), b - high_f32(high));
 }
 
-// A position in the ring.
+// A position in a ring, and how often it has been gone round.
 struct Slot {
   int slot = 0;
-  uint32_t phase = 0;
+  uint32_t wrap = 0;
+  __device__ __forceinline__ uint32_t phase() const { return wrap & 1; }
   __device__ __forceinline__ void next(int n) {
     if (++slot == n) {
       slot = 0;
-      phase ^= 1;
+      ++wrap;
     }
   }
 };
+
+// The barrier that tells of a stage's arrival belongs to the slot and to the
+// group that takes the stage: its phases are fills that this group takes, each
+// of which it waits for.  (With one barrier for both groups, a ring of an odd
+// number of slots gives the groups a slot's fills in turn, and a group would
+// tell its next fill from its last by a parity that the other group's fill,
+// not yet there, leaves unchanged.)  So a barrier's phase is the number of
+// times round where the groups have slots of their own, and half of it where
+// they have them in turn.
+template <int kGroups>
+__device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
+  return (kGroups == 2 && (slots & 1) ? wrap >> 1 : wrap) & 1;
+}
 
 // Or-reduction over the multiplying warps, all of which meet here.
 template <int kThreads>
@@ -271,7 +285,8 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
   using F = Format<kKind>;
   constexpr int kRows = F::kRows, kTiles = kRows / 16, kWarps = F::kGroups * 8, kThreads = kWarps * 32;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t full_w[kMaxStages], empty_w[kMaxStages], full_x[kMaxStages], empty_x[kMaxStages];
+  __shared__ uint64_t full_w[F::kGroups][kMaxStages], empty_w[kMaxStages];
+  __shared__ uint64_t full_x[F::kGroups][kMaxStages], empty_x[kMaxStages];
   __shared__ uint64_t item_full[kItems], item_done[kItems], item_empty[kItems];
   __shared__ int32_t item[kItems];
   __shared__ __align__(16) FewUnit unit_cache[kUnitCache];
@@ -282,11 +297,11 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&full_w[i], 1);
+      for (int j = 0; j < F::kGroups; ++j) mbar_init(&full_w[j][i], 1);
       mbar_init(&empty_w[i], 8);
     }
     for (int i = 0; i < a.row_stages; ++i) {
-      mbar_init(&full_x[i], 1);
+      for (int j = 0; j < F::kGroups; ++j) mbar_init(&full_x[j][i], 1);
       mbar_init(&empty_x[i], 8);
     }
     for (int i = 0; i < kItems; ++i) {
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
     for (int i = first_s;;) {
       int next = 0;
       if (lane == 0) next = atomicAdd(&p.header->ticket, 1);
-      ok = wait_warp(&item_empty[it.slot], it.phase ^ 1, abort);
+      ok = wait_warp(&item_empty[it.slot], it.phase() ^ 1, abort);
       if (!ok) break;
       if (lane == 0) {
         item[it.slot] = i < total ? i : -1;
@@ -340,10 +355,10 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       const int e = units[q.unit].expert, nkb = q.down ? kb2 : kb1;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int nk = min(kStageKb, nkb - kb0);
-        ok = wait_warp(&empty_w[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_w[st.slot], st.phase() ^ 1, abort);
         if (!ok) break;
         uint8_t* dst = ring + st.slot * a.stage_bytes;
-        uint64_t* bar = &full_w[st.slot];
+        uint64_t* bar = &full_w[issued % F::kGroups][st.slot];
         if (kKind == MOE_WEIGHTS_BF16) {
           // packed tiles of 128 (gate/up: 64 and 64) or down_bn rows of 64
           // values; two runs of kRows / 2 rows for each 64-index block
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       int never = 0;
       for (int j = min(issued, a.stages); j > 0; --j) {
         const int n = issued - j;
-        wait_warp(&full_w[n % a.stages], (n / a.stages) & 1, &never);
+        wait_warp(&full_w[n % F::kGroups][n % a.stages], fill_phase<F::kGroups>(n / a.stages, a.stages), &never);
       }
     }
   } else if (warp == kWarps + 1) {
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
     Slot st, it;
     int issued = 0, complete = -1;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase, abort);
+      ok = wait_warp(&item_full[it.slot], it.phase(), abort);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       __syncwarp();
@@ -447,9 +462,9 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       uint8_t* dst = ring + a.row_offset + (part * a.cap + j) * kPitch;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int bytes = min(kStageKb, nkb - kb0) * 128;
-        ok = wait_warp(&empty_x[st.slot], st.phase ^ 1, abort);
+        ok = wait_warp(&empty_x[st.slot], st.phase() ^ 1, abort);
         if (!ok) break;
-        uint64_t* bar = &full_x[st.slot];
+        uint64_t* bar = &full_x[issued % F::kGroups][st.slot];
         if (lane == 0) mbar_arrive_expect_tx(bar, n * parts * bytes);
         __syncwarp();
         if (src) bulk_load(dst + st.slot * a.row_stage_bytes, src + kb0 * 128, bytes, bar);
@@ -462,18 +477,19 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       int never = 0;
       for (int j = min(issued, a.row_stages); j > 0; --j) {
         const int n = issued - j;
-        wait_warp(&full_x[n % a.row_stages], (n / a.row_stages) & 1, &never);
+        wait_warp(&full_x[n % F::kGroups][n % a.row_stages], fill_phase<F::kGroups>(n / a.row_stages, a.row_stages),
+                  &never);
       }
     }
   } else if (warp == kWarps + 2) {
     // ------------------------------------------------ news of finished strips
     Slot it;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase, abort);
+      ok = wait_warp(&item_full[it.slot], it.phase(), abort);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       if (i >= 0 && i < products) {
-        ok = wait_warp(&item_done[it.slot], it.phase, abort);
+        ok = wait_warp(&item_done[it.slot], it.phase(), abort);
         if (!ok) break;
         const Piece q = piece_of(i, n_units, strips1, strips2, units);
         if (lane == 0) add_release(q.down ? p.strips + q.strip : p.ready + q.unit, 1);
@@ -494,7 +510,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       // A wait that ran out in one warp ends all of them, together: they meet
       // at the next or-reduction, one for each piece of a product and one at
       // the end, and none waits for a barrier that another does not reach.
-      if (ok) ok = wait_warp(&item_full[it.slot], it.phase, abort);
+      if (ok) ok = wait_warp(&item_full[it.slot], it.phase(), abort);
       if (!ok) {
         abort_s = 1;
         if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
@@ -541,8 +557,8 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       float acc[kTiles][2][4] = {};
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         if (turn == group) {
-          ok = wait_warp(&full_x[row_st.slot], row_st.phase, abort);
-          if (ok) ok = wait_warp(&full_w[st.slot], st.phase, abort);
+          ok = wait_warp(&full_x[group][row_st.slot], fill_phase<F::kGroups>(row_st.wrap, a.row_stages), abort);
+          if (ok) ok = wait_warp(&full_w[group][st.slot], fill_phase<F::kGroups>(st.wrap, a.stages), abort);
           if (!ok) {
             abort_s = 1;
             break;

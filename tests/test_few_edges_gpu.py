@@ -86,3 +86,21 @@ def test_gates_that_change_from_call_to_call():
     got = [moe.moe_forward_few(x, routes[i % 4], packed, E, k, f, workspace=ws, topk_idx=idx, topk_w=w) for i in range(40)]
     torch.cuda.synchronize()
     assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
+
+
+@pytest.mark.parametrize("T", [5, 6, 7, 8])
+def test_fp8_rings_of_three_slots(T):
+    """5 to 8 tokens leave room for three stages of rows (and of weights), which two groups of warps take in turn: the
+    same bits every time, whatever the caches hold, and the right ones."""
+    E, d, f, k = 6, 2048, 1024, 3
+    packed, mats = ref.weights("fp8", E, d, f)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    flush = torch.empty(64 << 20, device="cuda")
+    first = moe.moe_forward_few(x, logits, packed, E, k, f, weights="fp8")
+    ref.check(first, *ref.layer(x, *ref.route(logits, k), mats, "fp8"))
+    for i in range(60):
+        if i % 2:
+            flush.fill_(float(i))
+        assert torch.equal(moe.moe_forward_few(x, logits, packed, E, k, f, weights="fp8"), first)
