@@ -880,6 +880,30 @@ MOE_API moe_status_t moe_selftest_wait_timeout(void* workspace, size_t workspace
 MOE_API moe_status_t moe_selftest_steal_wait(int32_t* out, int64_t limit_ns, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Checks of what the kernels for a few tokens do when a wait runs out: the
+ * calls themselves, with waits that end after limit_ns (1 .. 2e9 ns) and
+ * with something that never comes.  No fault; the context stays usable.
+ *   moe_selftest_few_wait         moe_forward_few (renormalize 1), with one of
+ *     its T * k + ceil(d / 32) counters of finished pieces spoiled, so that the
+ *     wait for it never ends by itself: number u < T * k counts the finished
+ *     strips of unit u's h (there is a unit 0 always), T * k + s the units
+ *     finished with output strip s (s < d / 32, or d / 64 with coded weights).
+ *     -1: none, and only the limit ends a wait.  The status word then holds
+ *     MOE_ERR_TIMEOUT, and out is undefined.
+ *   moe_selftest_linear_int4_wait  moe_linear_int4, with rows of x fetched for
+ *     the first row_strips strips of 64 outputs alone: the outputs from
+ *     64 * row_strips on are NaN.
+ * Errors: those of the calls, and MOE_ERR_INVALID_ARG for the values above.
+ * ---------------------------------------------------------------------- */
+MOE_API moe_status_t moe_selftest_few_wait(const void* x, const float* logits, const void* packed, int32_t weights,
+                                           int32_t group, int64_t T, int32_t d, int32_t E, int32_t k, int32_t f,
+                                           void* out, void* workspace, size_t workspace_bytes, int64_t spoiled,
+                                           int64_t limit_ns, moe_stream_t stream);
+MOE_API moe_status_t moe_selftest_linear_int4_wait(const void* x, int64_t x_stride, const void* packed, int64_t M,
+                                                   int64_t K, int64_t N, int32_t group, void* out, int64_t out_stride,
+                                                   int32_t row_strips, int64_t limit_ns, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Reads the device status word at the start of a workspace used by
  * moe_dispatch_scan, moe_grouped_swiglu or moe_forward, after waiting for
  * `stream`.  *status receives MOE_OK or the first device error.

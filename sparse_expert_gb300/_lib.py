@@ -132,6 +132,8 @@ SIGNATURES = {
     "moe_linear_int4_packed_bytes": (_SZ, [_I64, _I64, _I32]),
     "moe_pack_linear_int4": (_S, [_P, _P, _I64, _I64, _I32, _P, _P]),
     "moe_linear_int4": (_S, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P]),
+    "moe_selftest_few_wait": (_S, [_P, _P, _P, _I32, _I32, _I64, _I32, _I32, _I32, _I32, _P, _P, _SZ, _I64, _I64, _P]),
+    "moe_selftest_linear_int4_wait": (_S, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _I32, _I64, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)
@@ -1309,4 +1311,30 @@ def moe_linear_int4(x, packed, N, group=128, out=None, stream=None):
                                  _raw_stream(index))
     if status:
         _check(status, "moe_linear_int4")
+    return out
+
+
+def moe_selftest_few_wait(x, logits, packed, E, k, f, weights, workspace, spoiled, limit_ns, group=128):
+    """moe_forward_few with waits of limit_ns and a counter of finished pieces (or -1: none) that is never reached; the
+    workspace's status word tells (moe_read_device_status)."""
+    index = _device_of(x, "x")
+    _out(logits, index, (x.shape[0], E), torch.float32, "logits")
+
+    def entry(x_ptr, l_ptr, p_ptr, kind, group, T, d, E, k, f, _, out_ptr, i_ptr, w_ptr, ws_ptr, size, stream):
+        return lib.moe_selftest_few_wait(x_ptr, l_ptr, p_ptr, kind, group, T, d, E, k, f, out_ptr, ws_ptr, size,
+                                         int(spoiled), int(limit_ns), stream)
+    return _forward_few(entry, "moe_selftest_few_wait", x, logits, logits.data_ptr(), packed, E, k, f, weights, group,
+                        True, workspace, None, None, None, index)
+
+
+def moe_selftest_linear_int4_wait(x, packed, N, row_strips, limit_ns, group=128):
+    """moe_linear_int4 with waits of limit_ns and rows of x for the first row_strips strips of 64 outputs alone."""
+    index = _device_of(x, "x")
+    x_stride = _rows(x, "x", index, None, torch.bfloat16)
+    M, K = x.shape
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    p_ptr = _packed_int4(packed, index, _linear_int4_bytes(K, N, group), group)
+    _check(lib.moe_selftest_linear_int4_wait(x.data_ptr(), x_stride, p_ptr, M, K, N, group, out.data_ptr(), N,
+                                             int(row_strips), int(limit_ns), _raw_stream(index)),
+           "moe_selftest_linear_int4_wait")
     return out

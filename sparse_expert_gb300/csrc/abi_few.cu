@@ -93,10 +93,12 @@ FewLayout few_layout(int64_t T, int32_t E, int32_t k, int32_t d, int32_t f) {
   return L;
 }
 
+// spoiled (of a check of the waits, else -1): a counter of finished pieces that
+// is set to what no number of pieces makes it.
 moe_status_t few(const void* x, const float* logits, const void* router, const void* packed, int32_t weights,
                  int32_t group, int64_t T, int32_t d, int32_t E, int32_t k, int32_t f, int32_t renormalize, void* out,
                  int32_t* topk_idx_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
-                 moe_stream_t stream) {
+                 moe_stream_t stream, int64_t spoiled = -1, uint64_t wait_ns = kWaitLimitNs) {
   moe_status_t s = check_few(T, E, k, d, f);
   if (s != MOE_OK) return s;
   switch (weights) {
@@ -153,6 +155,10 @@ moe_status_t few(const void* x, const float* logits, const void* router, const v
   r.n_counters = L.n_counters;
   cudaError_t e = launch_few_route(r, st);
   if (e != cudaSuccess) return cuda_fail(e, "route launch");
+  if (spoiled >= 0) {
+    e = cudaMemsetAsync(counters + spoiled, 0x80, sizeof(int32_t), st);
+    if (e != cudaSuccess) return cuda_fail(e, "counter");
+  }
   FewExperts p{};
   p.x = x;
   p.packed = packed;
@@ -172,8 +178,33 @@ moe_status_t few(const void* x, const float* logits, const void* router, const v
   p.h = ws + L.h;
   p.y = reinterpret_cast<float*>(ws + L.y);
   p.out = out;
+  p.wait_ns = wait_ns;
   e = launch_few_experts(p, dev.num_sms, st);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "experts launch");
+}
+
+// row_strips: strips of outputs that rows of x are fetched for (fewer than there are: a check of the waits).
+moe_status_t linear(const void* x, int64_t x_stride, const void* packed, int64_t M, int64_t K, int64_t N, int32_t group,
+                    void* out, int64_t out_stride, moe_stream_t stream, int32_t row_strips = INT32_MAX,
+                    uint64_t wait_ns = kWaitLimitNs) {
+  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M must not be negative");
+  if (M > MOE_LINEAR_INT4_MAX_ROWS) return fail(MOE_ERR_UNSUPPORTED, "M must be at most MOE_LINEAR_INT4_MAX_ROWS (16)");
+  moe_status_t s = check_int4_matrix(K, N, group);
+  if (s != MOE_OK || M == 0) return s;
+  if (!x || !packed || !out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (M > 1 && (x_stride < K || out_stride < N))
+    return fail(MOE_ERR_INVALID_ARG, "x_stride must be at least K and out_stride at least N");
+  if (!aligned(x, 16) || (M > 1 && x_stride % 8 != 0))
+    return fail(MOE_ERR_INVALID_ARG, "rows of x must be 16-byte aligned");
+  if (!aligned(packed, kAlign) || !aligned(out, 2))
+    return fail(MOE_ERR_INVALID_ARG, "packed must be 256-byte aligned, out 2-byte");
+  DeviceInfo dev;
+  if ((s = device_info(&dev)) != MOE_OK) return s;
+  const cudaError_t e =
+      launch_linear_int4(LinearInt4{x, x_stride, packed, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N),
+                                    group, out, out_stride, wait_ns, row_strips},
+                         dev.num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "linear launch");
 }
 
 }  // namespace
@@ -263,24 +294,31 @@ moe_status_t moe_pack_linear_int4(const uint8_t* codes, const void* scales, int6
 
 moe_status_t moe_linear_int4(const void* x, int64_t x_stride, const void* packed, int64_t M, int64_t K, int64_t N,
                              int32_t group, void* out, int64_t out_stride, moe_stream_t stream) {
-  if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M must not be negative");
-  if (M > MOE_LINEAR_INT4_MAX_ROWS) return fail(MOE_ERR_UNSUPPORTED, "M must be at most MOE_LINEAR_INT4_MAX_ROWS (16)");
-  moe_status_t s = check_int4_matrix(K, N, group);
-  if (s != MOE_OK || M == 0) return s;
-  if (!x || !packed || !out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
-  if (M > 1 && (x_stride < K || out_stride < N))
-    return fail(MOE_ERR_INVALID_ARG, "x_stride must be at least K and out_stride at least N");
-  if (!aligned(x, 16) || (M > 1 && x_stride % 8 != 0))
-    return fail(MOE_ERR_INVALID_ARG, "rows of x must be 16-byte aligned");
-  if (!aligned(packed, kAlign) || !aligned(out, 2))
-    return fail(MOE_ERR_INVALID_ARG, "packed must be 256-byte aligned, out 2-byte");
-  DeviceInfo dev;
-  if ((s = device_info(&dev)) != MOE_OK) return s;
-  const cudaError_t e =
-      launch_linear_int4(LinearInt4{x, x_stride, packed, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N),
-                                    group, out, out_stride},
-                         dev.num_sms, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "linear launch");
+  return linear(x, x_stride, packed, M, K, N, group, out, out_stride, stream);
+}
+
+moe_status_t moe_selftest_few_wait(const void* x, const float* logits, const void* packed, int32_t weights,
+                                   int32_t group, int64_t T, int32_t d, int32_t E, int32_t k, int32_t f, void* out,
+                                   void* workspace, size_t workspace_bytes, int64_t spoiled, int64_t limit_ns,
+                                   moe_stream_t stream) {
+  const moe_status_t s = check_few(T, E, k, d, f);
+  if (s != MOE_OK) return s;
+  if (limit_ns < 1 || limit_ns > static_cast<int64_t>(kWaitLimitNs))
+    return fail(MOE_ERR_INVALID_ARG, "limit_ns must be in [1, 2e9]");
+  if (spoiled < -1 || spoiled >= few_layout(T, E, k, d, f).n_counters)
+    return fail(MOE_ERR_INVALID_ARG, "spoiled must be -1 or the index of a counter");
+  return few(x, logits, nullptr, packed, weights, group, T, d, E, k, f, 1, out, nullptr, nullptr, workspace,
+             workspace_bytes, stream, spoiled, static_cast<uint64_t>(limit_ns));
+}
+
+moe_status_t moe_selftest_linear_int4_wait(const void* x, int64_t x_stride, const void* packed, int64_t M, int64_t K,
+                                           int64_t N, int32_t group, void* out, int64_t out_stride, int32_t row_strips,
+                                           int64_t limit_ns, moe_stream_t stream) {
+  if (limit_ns < 1 || limit_ns > static_cast<int64_t>(kWaitLimitNs))
+    return fail(MOE_ERR_INVALID_ARG, "limit_ns must be in [1, 2e9]");
+  if (row_strips < 0) return fail(MOE_ERR_INVALID_ARG, "row_strips must not be negative");
+  return linear(x, x_stride, packed, M, K, N, group, out, out_stride, stream, row_strips,
+                static_cast<uint64_t>(limit_ns));
 }
 
 }  // extern "C"

@@ -112,19 +112,6 @@ struct Slot {
   }
 };
 
-// The barrier that tells of a stage's arrival belongs to the slot and to the
-// group that takes the stage: its phases are fills that this group takes, each
-// of which it waits for.  (With one barrier for both groups, a ring of an odd
-// number of slots gives the groups a slot's fills in turn, and a group would
-// tell its next fill from its last by a parity that the other group's fill,
-// not yet there, leaves unchanged.)  So a barrier's phase is the number of
-// times round where the groups have slots of their own, and half of it where
-// they have them in turn.
-template <int kGroups>
-__device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
-  return (kGroups == 2 && (slots & 1) ? wrap >> 1 : wrap) & 1;
-}
-
 // Or-reduction over the multiplying warps, all of which meet here.
 template <int kThreads>
 __device__ __forceinline__ bool any_of(bool v) {
@@ -339,7 +326,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
     for (int i = first_s;;) {
       int next = 0;
       if (lane == 0) next = atomicAdd(&p.header->ticket, 1);
-      ok = wait_warp(&item_empty[it.slot], it.phase() ^ 1, abort);
+      ok = wait_warp(&item_empty[it.slot], it.phase() ^ 1, abort, p.wait_ns);
       if (!ok) break;
       if (lane == 0) {
         item[it.slot] = i < total ? i : -1;
@@ -355,7 +342,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       const int e = units[q.unit].expert, nkb = q.down ? kb2 : kb1;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int nk = min(kStageKb, nkb - kb0);
-        ok = wait_warp(&empty_w[st.slot], st.phase() ^ 1, abort);
+        ok = wait_warp(&empty_w[st.slot], st.phase() ^ 1, abort, p.wait_ns);
         if (!ok) break;
         uint8_t* dst = ring + st.slot * a.stage_bytes;
         uint64_t* bar = &full_w[issued % F::kGroups][st.slot];
@@ -408,21 +395,14 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       if (!ok) break;
       i = __shfl_sync(0xffffffffu, next, 0);
     }
-    if (!ok) {
-      // what is in flight has to land before the block may end
-      abort_s = 1;
-      int never = 0;
-      for (int j = min(issued, a.stages); j > 0; --j) {
-        const int n = issued - j;
-        wait_warp(&full_w[n % F::kGroups][n % a.stages], fill_phase<F::kGroups>(n / a.stages, a.stages), &never);
-      }
-    }
+    if (!ok) abort_s = 1;
+    wait_for_copies<F::kGroups>(full_w[0], kMaxStages, issued, a.stages);
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------ the tokens' rows
     Slot st, it;
     int issued = 0, complete = -1;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase(), abort);
+      ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       __syncwarp();
@@ -436,7 +416,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       if (q.down && complete != q.unit) {  // every strip of its h
         const uint64_t t0 = global_timer_ns();
         while (load_acquire(p.ready + q.unit) != strips1) {
-          if (*abort || global_timer_ns() - t0 > kWaitLimitNs) {
+          if (*abort || global_timer_ns() - t0 > p.wait_ns) {
             ok = false;
             break;
           }
@@ -462,7 +442,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       uint8_t* dst = ring + a.row_offset + (part * a.cap + j) * kPitch;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int bytes = min(kStageKb, nkb - kb0) * 128;
-        ok = wait_warp(&empty_x[st.slot], st.phase() ^ 1, abort);
+        ok = wait_warp(&empty_x[st.slot], st.phase() ^ 1, abort, p.wait_ns);
         if (!ok) break;
         uint64_t* bar = &full_x[issued % F::kGroups][st.slot];
         if (lane == 0) mbar_arrive_expect_tx(bar, n * parts * bytes);
@@ -472,24 +452,17 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
         st.next(a.row_stages);
       }
     }
-    if (!ok) {
-      abort_s = 1;
-      int never = 0;
-      for (int j = min(issued, a.row_stages); j > 0; --j) {
-        const int n = issued - j;
-        wait_warp(&full_x[n % F::kGroups][n % a.row_stages], fill_phase<F::kGroups>(n / a.row_stages, a.row_stages),
-                  &never);
-      }
-    }
+    if (!ok) abort_s = 1;
+    wait_for_copies<F::kGroups>(full_x[0], kMaxStages, issued, a.row_stages);
   } else if (warp == kWarps + 2) {
     // ------------------------------------------------ news of finished strips
     Slot it;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase(), abort);
+      ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       if (i >= 0 && i < products) {
-        ok = wait_warp(&item_done[it.slot], it.phase(), abort);
+        ok = wait_warp(&item_done[it.slot], it.phase(), abort, p.wait_ns);
         if (!ok) break;
         const Piece q = piece_of(i, n_units, strips1, strips2, units);
         if (lane == 0) add_release(q.down ? p.strips + q.strip : p.ready + q.unit, 1);
@@ -510,7 +483,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       // A wait that ran out in one warp ends all of them, together: they meet
       // at the next or-reduction, one for each piece of a product and one at
       // the end, and none waits for a barrier that another does not reach.
-      if (ok) ok = wait_warp(&item_full[it.slot], it.phase(), abort);
+      if (ok) ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) {
         abort_s = 1;
         if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
@@ -532,7 +505,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
         const uint64_t begin = global_timer_ns();
         for (int s = col0 / kRows; s * kRows < col0 + kSumCols; ++s)
           while (ok && load_acquire(p.strips + s) != n_units)
-            if (*abort || global_timer_ns() - begin > kWaitLimitNs) ok = false;
+            if (*abort || global_timer_ns() - begin > p.wait_ns) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         for (int o = threadIdx.x; o < kSumCols * min(kSumTokens, p.T - t0); o += kThreads) {
@@ -557,8 +530,9 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       float acc[kTiles][2][4] = {};
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         if (turn == group) {
-          ok = wait_warp(&full_x[group][row_st.slot], fill_phase<F::kGroups>(row_st.wrap, a.row_stages), abort);
-          if (ok) ok = wait_warp(&full_w[group][st.slot], fill_phase<F::kGroups>(st.wrap, a.stages), abort);
+          ok = wait_warp(&full_x[group][row_st.slot], fill_phase<F::kGroups>(row_st.wrap, a.row_stages), abort,
+                         p.wait_ns);
+          if (ok) ok = wait_warp(&full_w[group][st.slot], fill_phase<F::kGroups>(st.wrap, a.stages), abort, p.wait_ns);
           if (!ok) {
             abort_s = 1;
             break;

@@ -62,9 +62,34 @@ __device__ __forceinline__ void mma_bf16_from(float (&d)[4], const float (&c)[4]
 
 // mbar_wait_warp for waits that are often over already: the clock is read only
 // where the first look fails.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return true;
-  return mbar_wait_warp(bar, parity, abort);
+  return mbar_wait_warp(bar, parity, abort, limit_ns);
+}
+
+// The barrier that tells of a stage's arrival belongs to the slot and to the
+// group that takes the stage: its phases are fills that this group takes, each
+// of which it waits for.  (With one barrier for both groups, a ring of an odd
+// number of slots gives the groups a slot's fills in turn, and a group would
+// tell its next fill from its last by a parity that the other group's fill,
+// not yet there, leaves unchanged.)  So a barrier's phase is the number of
+// times round where the groups have slots of their own, and half of it where
+// they have them in turn.
+template <int kGroups>
+__device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
+  return (kGroups == 2 && (slots & 1) ? wrap >> 1 : wrap) & 1;
+}
+
+// The last thing that a fetching warp does, whether or not it fetched
+// everything: waits until what it has in flight has landed (`issued` stages so
+// far, into a ring of `slots`; full [kGroups][pitch]).  Its own work may be
+// over while another warp gives up, and shared memory that a copy is still
+// going to write must not pass to another block.
+template <int kGroups>
+__device__ __forceinline__ void wait_for_copies(uint64_t* full, int pitch, int issued, int slots) {
+  int never = 0;
+  for (int n = issued < slots ? 0 : issued - slots; n < issued; ++n)
+    wait_warp(&full[n % kGroups * pitch + n % slots], fill_phase<kGroups>(n / slots, slots), &never, kWaitLimitNs);
 }
 
 }  // namespace moe

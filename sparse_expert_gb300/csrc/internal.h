@@ -333,6 +333,7 @@ struct FewExperts {
   void* h;               // [T*k, f] bf16
   float* y;              // [T*k, d]
   void* out;             // [T, d] bf16
+  uint64_t wait_ns;      // limit of a wait
 };
 cudaError_t launch_few_experts(const FewExperts& p, int num_sms, cudaStream_t stream);
 
@@ -354,6 +355,8 @@ struct LinearInt4 {
   int M, K, N, group;
   void* out;      // [M] rows of N bf16
   int64_t out_stride;
+  uint64_t wait_ns;  // limit of a wait
+  int row_strips;    // strips of kInt4Rows outputs that rows of x are fetched for: all, but in a check of the waits
 };
 cudaError_t launch_linear_int4(const LinearInt4& p, int num_sms, cudaStream_t stream);
 
