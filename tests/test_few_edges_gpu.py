@@ -104,3 +104,132 @@ def test_fp8_rings_of_three_slots(T):
         if i % 2:
             flush.fill_(float(i))
         assert torch.equal(moe.moe_forward_few(x, logits, packed, E, k, f, weights="fp8"), first)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T,E,k", [(64, 20, 9), (64, 64, 32), (17, 33, 31), (64, 1024, 32)])
+def test_more_pairs_than_units_kept_in_shared_memory(kind, T, E, k):
+    """T * k > 512; with 1,024 experts nearly every pair is a unit."""
+    d = f = 128
+    packed, mats = ref.weights(kind, E, d, f)
+    gen = torch.Generator(device="cuda").manual_seed(T + k)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    out = moe.moe_forward_few(x, logits, packed, E, k, f, weights=kind)
+    idx, w = ref.route(logits, k)
+    ref.check(out, *ref.layer(x, idx, w, mats, kind))
+
+
+@pytest.mark.parametrize("T", [2, 13])
+def test_subnormal_fp8_codes(T):
+    """Weights of subnormal E4M3 codes (0x01 to 0x07 and their negatives) alone, with scales that make them matter."""
+    E, d, f, k = 4, 256, 128, 2
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    coded, mats = [], []
+    for K, N in ((d, f), (d, f), (f, d)):
+        codes = torch.randint(1, 8, (E, K, N), generator=gen, device="cuda", dtype=torch.uint8)
+        codes |= torch.randint(0, 2, (E, K, N), generator=gen, device="cuda", dtype=torch.uint8) << 7
+        scales = torch.exp(0.2 * torch.randn(E * K * N // 128, generator=gen, device="cuda")) * (2.0 ** 7 / math.sqrt(K))
+        coded.append((codes, scales))
+        mats.append(ref.dequantize_fp8(codes, scales, (E, K, N)))
+    packed = moe.moe_pack_weights_fp8(*coded, E, d, f)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    out = moe.moe_forward_few(x, logits, packed, E, k, f, weights="fp8")
+    idx, w = ref.route(logits, k)
+    want, bound = ref.layer(x, idx, w, mats, "fp8")
+    ref.check(out, want, bound)
+    assert float((want.abs() > 10 * bound).double().mean()) > 0.5  # a lost code would be seen
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_experts_near_moe_forward(group):
+    """4-bit experts beside the layer's other form on the same weights in bf16."""
+    E, d, f, T, k = 16, 512, 256, 20, 4
+    packed, mats = ref.weights("int4", E, d, f, group)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    a = moe.moe_forward(x, logits, moe.moe_pack_weights(*[m.to(torch.bfloat16) for m in mats]), E, k, f)
+    b = moe.moe_forward_few(x, logits, packed, E, k, f, weights="int4", group=group)
+    rel = float((a.float() - b.float()).norm() / b.float().norm())
+    # gate, up and down weights, h, y and out rounded on one side, out on the other: seven roundings, each U / sqrt(3)
+    # in the mean over evenly spread values
+    assert rel <= 1.25 * 7 ** 0.5 * ref.U / 3.0 ** 0.5
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,f", [(65536, 128), (128, 65536)])
+def test_longest_rows(kind, d, f):
+    E, T, k = 2, 18, 2
+    packed, mats = ref.weights(kind, E, d, f, seed=6)
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    out = moe.moe_forward_few(x, logits, packed, E, k, f, weights=kind)
+    ref.check(out, *ref.layer(x, *ref.route(logits, k), mats, kind))
+
+
+def test_routed_by_the_longest_rows():
+    E, T, k, d, f = 6, 5, 2, 65536, 64
+    packed, mats = ref.weights("bf16", E, d, f, seed=7)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    w_router = (torch.randn(d, E, generator=gen, device="cuda") / d ** 0.5).to(torch.bfloat16)
+    logits = x.double() @ w_router.double()
+    # 64 additions inside a K block, d / 1024 blocks a warp, 16 warps; any of them may cut off
+    d_logit = float(((80 + d / 1024) * 2.0 ** -23 * (x.double().abs() @ w_router.double().abs())).max())
+    top = torch.sort(logits, dim=1, descending=True)[0]
+    assert (top[:, :k] - top[:, 1:k + 1]).min() > 2 * d_logit, "these inputs do not tell which experts are right"
+    out = moe.moe_forward_few_routed(x, moe.moe_pack_router_weights(w_router), packed, E, k, f)
+    ref.check(out, *ref.layer(x, *ref.route(logits, k), mats, "bf16", d_logit))
+
+
+@pytest.mark.parametrize("kind,E", [("bf16", 300), ("fp8", 600), ("int4", 1000)])
+def test_experts_beyond_32_bits(kind, E):
+    """The last experts of a layer whose gate and up weights alone take more than 2^32 bytes."""
+    d = f = 2048
+    chosen, T, k = [E - 1, E // 2, 1], 4, 2
+    gen = torch.Generator(device="cuda").manual_seed(E)
+    mats = [(torch.randn(3, d, f, generator=gen, device="cuda") / d ** 0.5).to(torch.bfloat16) for _ in range(3)]
+
+    def spread(values, at):  # the chosen experts' values among others that are never read
+        full = torch.zeros(E, *values.shape[1:], dtype=values.dtype, device="cuda")
+        full[chosen] = values
+        return full.reshape(-1) if at else full
+    if kind == "bf16":
+        packed = moe.moe_pack_weights(*[spread(m, 0) for m in mats])
+        mats = [m.double() for m in mats]
+    elif kind == "fp8":
+        coded = [moe.moe_quantize_fp8_blockwise(m) for m in mats]
+        mats = [ref.dequantize_fp8(c, s, (3, d, f)) for c, s in coded]
+        packed = moe.moe_pack_weights_fp8(*[(spread(c.view(torch.uint8).reshape(3, d, f), 0), spread(s.reshape(3, -1), 1))
+                                            for c, s in coded], E, d, f)
+    else:
+        coded = [moe.moe_quantize_int4(m) for m in mats]
+        mats = [ref.dequantize_int4(c, s, 128) for c, s in coded]
+        packed = moe.moe_pack_weights_int4(*[(spread(c, 0), spread(s, 0)) for c, s in coded], E, d, f)
+    assert packed.numel() * packed.element_size() > 1.5 * 2 ** 32
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    few_logits = torch.randn(T, 3, generator=gen, device="cuda")
+    logits = torch.full((T, E), -40.0, device="cuda")
+    logits[:, chosen] = few_logits
+    out = moe.moe_forward_few(x, logits, packed, E, k, f, weights=kind)
+    ref.check(out, *ref.layer(x, *ref.route(few_logits, k), mats, kind))
+
+
+def test_matrix_beyond_32_bits():
+    """The last columns of a 4-bit matrix of more than 2^32 bytes."""
+    K, N, M, last = 65536, 140_003, 3, 1000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (K // 2, N), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.rand(K // 128, N, generator=gen, device="cuda").to(torch.bfloat16)
+    packed = moe.moe_pack_linear_int4(codes, scales, K, N)
+    assert packed.numel() > 2 ** 32
+    x = torch.randn(M, K, generator=gen, device="cuda").to(torch.bfloat16)
+    out = moe.moe_linear_int4(x, packed, N)
+    for part in (slice(0, last), slice(N // 2, N // 2 + last), slice(N - last, N)):
+        w = ref.dequantize_int4(codes[:, part].contiguous(), scales[:, part], 128)
+        want = x.double() @ w
+        size = x.double().abs() @ (8.0 * scales[:, part].double().repeat_interleave(128, 0))
+        ref.check(out[:, part], want, ref.U * want.abs() + 7.0 * ref.gamma(K) * size)
