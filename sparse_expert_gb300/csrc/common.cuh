@@ -89,10 +89,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // Same, taken by a whole warp with a warp-uniform outcome (needed before
-// .sync.aligned instructions).
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                               uint64_t limit_ns = kWaitLimitNs) {
-  const uint32_t a = smem_addr(bar);
+// .sync.aligned instructions).  a: the barrier's shared address.
+__device__ __forceinline__ bool mbar_wait_warp_at(uint32_t a, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit_ns) {
   uint64_t t0 = 0;
   const int lane = threadIdx.x & 31;
   if (lane == 0) t0 = global_timer_ns();
@@ -105,6 +104,11 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
       if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
     }
   }
+}
+
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               uint64_t limit_ns = kWaitLimitNs) {
+  return mbar_wait_warp_at(smem_addr(bar), parity, abort, limit_ns);
 }
 
 // try_wait with a suspend-time hint: a thread whose phase is not complete is

@@ -99,15 +99,17 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& high, uin
   low = pack_bf16x2(a - low_f32(high), b - high_f32(high));
 }
 
-// A position in a ring, and how often it has been gone round.
+// A position in a ring, and how often it has been gone round (or, without
+// kCount, whether that is an odd number).
+template <bool kCount = false>
 struct Slot {
   int slot = 0;
   uint32_t wrap = 0;
-  __device__ __forceinline__ uint32_t phase() const { return wrap & 1; }
+  __device__ __forceinline__ uint32_t phase() const { return kCount ? wrap & 1 : wrap; }
   __device__ __forceinline__ void next(int n) {
     if (++slot == n) {
       slot = 0;
-      ++wrap;
+      wrap = kCount ? wrap + 1 : wrap ^ 1;
     }
   }
 };
@@ -321,12 +323,12 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
 
   if (warp == kWarps) {
     // ------------------------------------------------ weights
-    Slot st, it;
+    Slot<> st, it;
     int issued = 0;
     for (int i = first_s;;) {
       int next = 0;
       if (lane == 0) next = atomicAdd(&p.header->ticket, 1);
-      ok = wait_warp(&item_empty[it.slot], it.phase() ^ 1, abort, p.wait_ns);
+      ok = wait_warp<true>(&item_empty[it.slot], it.phase() ^ 1, abort, p.wait_ns);
       if (!ok) break;
       if (lane == 0) {
         item[it.slot] = i < total ? i : -1;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       const int e = units[q.unit].expert, nkb = q.down ? kb2 : kb1;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int nk = min(kStageKb, nkb - kb0);
-        ok = wait_warp(&empty_w[st.slot], st.phase() ^ 1, abort, p.wait_ns);
+        ok = wait_warp<true>(&empty_w[st.slot], st.phase() ^ 1, abort, p.wait_ns);
         if (!ok) break;
         uint8_t* dst = ring + st.slot * a.stage_bytes;
         uint64_t* bar = &full_w[issued % F::kGroups][st.slot];
@@ -396,13 +398,13 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       i = __shfl_sync(0xffffffffu, next, 0);
     }
     if (!ok) abort_s = 1;
-    wait_for_copies<F::kGroups>(full_w[0], kMaxStages, issued, a.stages);
+    wait_for_copies<F::kGroups, true>(full_w[0], kMaxStages, issued, a.stages);
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------ the tokens' rows
-    Slot st, it;
+    Slot<> st, it;
     int issued = 0, complete = -1;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
+      ok = wait_warp<true>(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       __syncwarp();
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       uint8_t* dst = ring + a.row_offset + (part * a.cap + j) * kPitch;
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         const int bytes = min(kStageKb, nkb - kb0) * 128;
-        ok = wait_warp(&empty_x[st.slot], st.phase() ^ 1, abort, p.wait_ns);
+        ok = wait_warp<true>(&empty_x[st.slot], st.phase() ^ 1, abort, p.wait_ns);
         if (!ok) break;
         uint64_t* bar = &full_x[issued % F::kGroups][st.slot];
         if (lane == 0) mbar_arrive_expect_tx(bar, n * parts * bytes);
@@ -453,16 +455,16 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       }
     }
     if (!ok) abort_s = 1;
-    wait_for_copies<F::kGroups>(full_x[0], kMaxStages, issued, a.row_stages);
+    wait_for_copies<F::kGroups, true>(full_x[0], kMaxStages, issued, a.row_stages);
   } else if (warp == kWarps + 2) {
     // ------------------------------------------------ news of finished strips
-    Slot it;
+    Slot<> it;
     while (ok) {
-      ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
+      ok = wait_warp<true>(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) break;
       const int i = *reinterpret_cast<volatile int32_t*>(&item[it.slot]);
       if (i >= 0 && i < products) {
-        ok = wait_warp(&item_done[it.slot], it.phase(), abort, p.wait_ns);
+        ok = wait_warp<true>(&item_done[it.slot], it.phase(), abort, p.wait_ns);
         if (!ok) break;
         const Piece q = piece_of(i, n_units, strips1, strips2, units);
         if (lane == 0) add_release(q.down ? p.strips + q.strip : p.ready + q.unit, 1);
@@ -476,14 +478,15 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
   } else {
     // ------------------------------------------------ products
     const int group = warp >> 3, kb_own = warp & 7, g = lane >> 2, t = lane & 3;
-    Slot st, row_st, it;
+    Slot<F::kGroups == 2> st, row_st;
+    Slot<> it;
     int turn = 0, buffer = 0;  // of the groups; of the sums
     float* const reduce = reinterpret_cast<float*>(ring + a.reduce_offset);  // [2][8 warps][kRows][8]
     for (;;) {
       // A wait that ran out in one warp ends all of them, together: they meet
       // at the next or-reduction, one for each piece of a product and one at
       // the end, and none waits for a barrier that another does not reach.
-      if (ok) ok = wait_warp(&item_full[it.slot], it.phase(), abort, p.wait_ns);
+      if (ok) ok = wait_warp<true>(&item_full[it.slot], it.phase(), abort, p.wait_ns);
       if (!ok) {
         abort_s = 1;
         if (F::kGroups == 2 && group == 0) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + kb_own) : "memory");
@@ -514,9 +517,9 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
 #pragma unroll 8
           for (int j = 0; j < p.k; ++j) {
             // written by the previous launch while this one's blocks are
-            // already there: not for the read-only path
-            const float w = __ldcg(p.topk_w + token * p.k + j);
-            const int row = __ldcg(p.pair_row + token * p.k + j);
+            // already there: plain loads, not the read-only path
+            const float w = p.topk_w[token * p.k + j];
+            const int row = p.pair_row[token * p.k + j];
             s = fmaf(w, __ldcg(p.y + static_cast<int64_t>(row) * p.d + n), s);
           }
           static_cast<__nv_bfloat16*>(p.out)[static_cast<int64_t>(token) * p.d + n] = __float2bfloat16_rn(s);
@@ -530,9 +533,10 @@ __global__ void __launch_bounds__((Format<kKind>::kGroups * 8 + 3) * 32, 1) few_
       float acc[kTiles][2][4] = {};
       for (int kb0 = 0; kb0 < nkb; kb0 += kStageKb) {
         if (turn == group) {
-          ok = wait_warp(&full_x[group][row_st.slot], fill_phase<F::kGroups>(row_st.wrap, a.row_stages), abort,
+          ok = wait_warp<true>(&full_x[group][row_st.slot], fill_phase<F::kGroups>(row_st.wrap, a.row_stages), abort,
                          p.wait_ns);
-          if (ok) ok = wait_warp(&full_w[group][st.slot], fill_phase<F::kGroups>(st.wrap, a.stages), abort, p.wait_ns);
+          if (ok)
+            ok = wait_warp<true>(&full_w[group][st.slot], fill_phase<F::kGroups>(st.wrap, a.stages), abort, p.wait_ns);
           if (!ok) {
             abort_s = 1;
             break;

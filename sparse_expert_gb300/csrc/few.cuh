@@ -61,9 +61,19 @@ __device__ __forceinline__ void mma_bf16_from(float (&d)[4], const float (&c)[4]
 }
 
 // mbar_wait_warp for waits that are often over already: the clock is read only
-// where the first look fails.
+// where the first look fails.  kCalled: what follows that look is a call.  The
+// expert kernel has a dozen of them and stalls for instructions otherwise (4 bits, 48
+// tokens of the 7B-A1B layer: 140 us, 146 with all of them inlined);
+// moe_linear_int4's has fewer and loses by it (13 x 6144 x 128001: 162 us, 169
+// with calls).
+template <int = 0>
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return mbar_wait_warp_at(bar, parity, abort, limit_ns);
+}
+template <bool kCalled>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   if (__all_sync(0xffffffffu, mbar_try_wait(smem_addr(bar), parity))) return true;
+  if constexpr (kCalled) return wait_longer(smem_addr(bar), parity, abort, limit_ns);
   return mbar_wait_warp(bar, parity, abort, limit_ns);
 }
 
@@ -77,7 +87,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // they have them in turn.
 template <int kGroups>
 __device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
-  return (kGroups == 2 && (slots & 1) ? wrap >> 1 : wrap) & 1;
+  return kGroups == 1 ? wrap & 1 : (slots & 1 ? wrap >> 1 : wrap) & 1;
 }
 
 // The last thing that a fetching warp does, whether or not it fetched
@@ -85,11 +95,12 @@ __device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
 // far, into a ring of `slots`; full [kGroups][pitch]).  Its own work may be
 // over while another warp gives up, and shared memory that a copy is still
 // going to write must not pass to another block.
-template <int kGroups>
+template <int kGroups, bool kCalled>
 __device__ __forceinline__ void wait_for_copies(uint64_t* full, int pitch, int issued, int slots) {
   int never = 0;
   for (int n = issued < slots ? 0 : issued - slots; n < issued; ++n)
-    wait_warp(&full[n % kGroups * pitch + n % slots], fill_phase<kGroups>(n / slots, slots), &never, kWaitLimitNs);
+    wait_warp<kCalled>(&full[n % kGroups * pitch + n % slots], fill_phase<kGroups>(n / slots, slots), &never,
+                       kWaitLimitNs);
 }
 
 }  // namespace moe

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
     int issued = 0;
     for (int strip = first; strip < a.strips && ok; strip += step)
       for (int u = unit0; u < unit1; u += kStageUnits) {
-        ok = wait_warp(&empty_w[st.slot], st.phase ^ 1, abort, p.wait_ns);
+        ok = wait_warp<false>(&empty_w[st.slot], st.phase ^ 1, abort, p.wait_ns);
         if (!ok) break;
         if (lane == 0) {
           const int bytes = min(kStageUnits, unit1 - u) * record;
@@ -91,14 +91,14 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
         st.next(kStages);
       }
     if (!ok) abort_s = 1;
-    wait_for_copies<1>(full_w, kStages, issued, kStages);
+    wait_for_copies<1, false>(full_w, kStages, issued, kStages);
   } else if (warp == kWarps + 1) {
     Slot st;
     int issued = 0;
     const uint8_t* src = lane < p.M ? static_cast<const uint8_t*>(p.x) + lane * p.x_stride * 2 : nullptr;
     for (int strip = first; strip < p.row_strips && ok; strip += step)
       for (int u = unit0; u < unit1; u += kStageUnits) {
-        ok = wait_warp(&empty_x[st.slot], st.phase ^ 1, abort, p.wait_ns);
+        ok = wait_warp<false>(&empty_x[st.slot], st.phase ^ 1, abort, p.wait_ns);
         if (!ok) break;
         const int k0 = u * kInt4Unit, bytes = 2 * (min(p.K, min(unit1, u + kStageUnits) * kInt4Unit) - k0);
         if (lane == 0) mbar_arrive_expect_tx(&full_x[st.slot], p.M * bytes);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
         st.next(kRowStages);
       }
     if (!ok) abort_s = 1;
-    wait_for_copies<1>(full_x, kRowStages, issued, kRowStages);
+    wait_for_copies<1, false>(full_x, kRowStages, issued, kRowStages);
   } else {
     const int g = lane >> 2, t = lane & 3;
     const bool two = p.M > 8;
@@ -119,8 +119,8 @@ __global__ void __launch_bounds__((kWarps + 2) * 32, 2) linear_int4_kernel(const
     for (int strip = first; strip < a.strips; strip += step) {
       float acc[4][2][4] = {};
       for (int u = unit0; u < unit1 && ok; u += kStageUnits) {
-        ok = wait_warp(&full_x[row_st.slot], row_st.phase, abort, p.wait_ns);
-        if (ok) ok = wait_warp(&full_w[st.slot], st.phase, abort, p.wait_ns);
+        ok = wait_warp<false>(&full_x[row_st.slot], row_st.phase, abort, p.wait_ns);
+        if (ok) ok = wait_warp<false>(&full_w[st.slot], st.phase, abort, p.wait_ns);
         if (!ok) {
           abort_s = 1;
           break;
