@@ -473,12 +473,12 @@ MOE_API moe_status_t moe_forward_routed(const void* x, const void* router_packed
 
 /* ------------------------------------------------------------------------
  * The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS), the form of a
- * serving step: two launches, the time that of reading the weights of the
- * experts that some token chose (the other experts' are not read).
+ * serving step: two launches, which read the weights of the experts that some
+ * token chose and no others.
  *   moe_forward_few         routes by logits [T, E] fp32, as moe_forward;
  *   moe_forward_few_routed  by x and moe_pack_router_weights' weights (E <= 512,
- *                           16-byte aligned): fp32 logits, within 2e-7 of the
- *                           largest partial sums.
+ *                           16-byte aligned): fp32 logits, within (80 + d / 1024)
+ *                           2^-23 of their sum of |x| |w| at worst.
  *   x [T, d] bf16; out [T, d] bf16 out; renormalize, topk_idx_out and
  *   topk_w_out (both optional) as moe_forward.  Selection, ties and gates are
  *   moe_route_topk's.
@@ -488,20 +488,27 @@ MOE_API moe_status_t moe_forward_routed(const void* x, const void* router_packed
  *                       finite).  The weight is E4M3 value x scale, not rounded
  *                       to bf16 on the way (moe_forward_fp8 does): the scale is
  *                       multiplied into the inputs instead, and those products
- *                       are rounded to bf16;
+ *                       are kept as two bf16 (a value and what its rounding
+ *                       left: 16 bits).  They have to stay below 2^67 in size:
+ *                       beyond, the token's output is infinite or NaN.  Products
+ *                       of a weight and an input below 2^-66 may be lost;
  *     MOE_WEIGHTS_INT4  moe_pack_weights_int4's with the same `group` (d and f
  *                       multiples of 128).  The weight is (code - 8) x scale;
  *                       codes are multiplied exactly, scales enter in fp32.
+ *                       Inputs (x and h) have to stay below 2^118 in size and
+ *                       scales below 2^126; an infinite input makes the token's
+ *                       output NaN.
  *   group    of 4-bit weights, the one that they were packed with (packed
  *            weights do not say it: with another one they are read as other
  *            weights, up to 9 % beyond the end of a shorter buffer); not looked at
  *            for the others.
- * h = silu(gate) * up is rounded to bf16, as everywhere in the layer; sums,
- * gates and the experts' outputs stay fp32 until out is rounded.  Results are
- * the same bits every time.  Logits must be finite (an expert with a logit of
+ * h = silu(gate) * up is kept as two bf16 (16 bits; moe_forward rounds it to
+ * one); sums, gates and the experts' outputs stay fp32 until out is rounded.
+ * Results are the same bits every time.  Logits must be finite (an expert with a logit of
  * -infinity is not chosen while k others are finite).
  * moe_forward_few_workspace_bytes gives 0 for sizes outside the range.  A
- * wait that ran out sets MOE_ERR_TIMEOUT in the workspace's status word.
+ * wait that ran out sets MOE_ERR_TIMEOUT in the workspace's status word, and
+ * out is then undefined.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE,
  *         MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
  * ---------------------------------------------------------------------- */
@@ -527,8 +534,8 @@ MOE_API moe_status_t moe_forward_few_routed(const void* x, const void* router_pa
  *          output (32, 64 or 128; the last group may be shorter);
  * and its weights are (code - 8) x scale.  K is a multiple of 8 up to 65536,
  * N any up to 2^24.
- * moe_quantize_int4: codes and scales of `matrices` matrices [K, N] of bf16,
- *   one after the other.  scale = bf16(amax / 7) (1 where that is 0), code =
+ * moe_quantize_int4: codes and scales of `matrices` matrices [K, N] of finite
+ *   bf16, one after the other.  scale = bf16(amax / 7) (1 where that is 0), code =
  *   8 + w / scale rounded to nearest even, within 0 .. 15.
  * moe_pack_weights_int4: experts' codes and scales (gate, up: [E] matrices
  *   [d, f]; down: [f, d]; d and f multiples of 128) in the layout that
@@ -540,7 +547,10 @@ MOE_API moe_status_t moe_forward_few_routed(const void* x, const void* router_pa
  *     out[m, :] = bf16(x[m, :] @ w),  0 <= M <= MOE_LINEAR_INT4_MAX_ROWS,
  *   x [M, K] bf16 with x_stride values between rows (rows 16-byte aligned),
  *   out [M, N] bf16 with out_stride.  Codes are multiplied exactly, sums and
- *   scales are fp32, out is rounded once.  The same bits every time.
+ *   scales are fp32, out is rounded once.  The same bits every time.  x has to
+ *   stay below 2^118 in size and scales below 2^126; an infinity in a row of x
+ *   makes that row of out NaN.  There is no status word: a wait that ran out
+ *   leaves NaN in the outputs that it concerns.
  * The sizes are 0 outside the range.  Errors: MOE_ERR_INVALID_ARG,
  * MOE_ERR_UNSUPPORTED, MOE_ERR_NO_DEVICE, MOE_ERR_CUDA.
  * ---------------------------------------------------------------------- */

@@ -50,9 +50,11 @@ constexpr size_t kSmemMost = 227 * 1024 - 1024 - sizeof(FewUnit) * kUnitCache;  
 // kGroups-th stage), and the padding of a token's row, with which the eight lanes that a 16-byte
 // shared load serves at once meet different banks: two rows of 64 bytes 64
 // apart, or, where a lane reads 32 bytes, 16 apart.
-// Groups, one or two, as measured (us): bf16 1T layer, 4 tokens, 388 and 408;
-// FP8 1T layer, 32 tokens, 1,717 and 1,550; 4 bits 7B-A1B layer, 48 tokens, 144
-// and 200 (two groups leave 96 registers a thread, and that kernel spills).
+// Groups, one or two, as measured (us), for one token and for more of them:
+// bf16 7B-A1B layer 35.2 and 37.1 (1), 215 and 229 (64), 1T layer 391 and 412
+// (4); FP8 7B-A1B layer 34.7 and 34.1 (1), 1T layer 1,727 and 1,564 (32); 4 bits
+// 1T layer 77.8 and 81.0 (1), 7B-A1B layer 146 and 199 (48; two groups leave 96
+// registers a thread, and that kernel spills).
 template <int kKind>
 struct Format;
 template <>
@@ -195,8 +197,10 @@ struct Multiply<MOE_WEIGHTS_BF16> {
 // E4M3 codes become bf16 by moving their bits: the code's sign, four exponent
 // bits and three mantissa bits at bf16's places are the code's value times
 // 2^-120, exactly, subnormal codes included.  The inputs carry 2^60 against
-// that, and the sums the other 2^60 at the end, so neither side leaves the
-// range.  Scales belong to an inner index (and 128 output features), so they
+// that, and the sums the other 2^60 at the end: inputs times scale may be up to
+// 2^67 in size, and products go down to 2^-66 before they lose bits.  (Beyond,
+// the value is infinite and its remainder NaN: to test for that here takes the
+// batch of 32 tokens from 1,551 to 1,602-1,644 us.)  Scales belong to an inner index (and 128 output features), so they
 // are multiplied into the inputs, once for all rows of the strip; the fp32
 // products enter as two bf16 each, which keeps 16 bits of them.
 constexpr float kFp8Lift = 1.152921504606846976e18f;  // 2^60

@@ -22,10 +22,10 @@ constexpr int kPartialPitch = kRouterTokens + 1;
 constexpr size_t kRouterSmem = sizeof(float) * kWarps * 32 * kPartialPitch;
 
 // Logits of the block's experts: [T, E_pad / 16] of x @ w_router, each warp
-// a share of the 64-value K blocks.  A K block's products are added by the
-// tensor cores, the K blocks and the warps in fp32 registers, rounded to
-// nearest: a block's sum is a fraction of the logit, so what the tensor cores
-// cut off is too, and the logits come out within about 2e-7 of their size.
+// a share of the 64-value K blocks.  A K block's 64 products are added by the
+// tensor cores, which may cut off, the d / 1024 K blocks of a warp and the 16
+// warps in fp32 registers, rounded to nearest: at most 2^-23 of the sum of
+// |x| |w| for each of the 80 + d / 1024 additions that a product goes through.
 __device__ __forceinline__ void router_logits(const FewRoute& p, float* partial) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int experts = p.E_pad / kRouterBlocks, e0 = static_cast<int>(cluster_rank()) * experts;

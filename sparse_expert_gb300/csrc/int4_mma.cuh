@@ -101,9 +101,9 @@ __device__ __forceinline__ void int4_block_of(float (&acc)[4][2][4], const uint8
 }
 
 // The same by how many scales and parts there are, which no block changes: the
-// forms have no tests inside (48 tokens of the 7B-A1B layer: 144 us, 152 with
-// them; moe_linear_int4's kernel has fewer registers and is better off with
-// one form, 162 us where forms give 170).
+// forms have no tests inside, which took 48 tokens of the 7B-A1B layer from 152
+// to 144 us (moe_linear_int4's kernel has fewer registers and is better off
+// with one form, 162 us where forms give 170).
 template <bool kTwo>
 __device__ __forceinline__ void int4_block(float (&acc)[4][2][4], const uint8_t* w, const uint8_t* scales, int groups,
                                            const uint8_t* const (&rows)[2], int low, int lane, int chunks = 8) {

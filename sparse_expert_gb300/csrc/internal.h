@@ -330,7 +330,7 @@ struct FewExperts {
   int32_t* strips;       // for each strip of outputs: finished units
   const float* topk_w;
   const int32_t* pair_row;
-  void* h;               // [T*k, f] bf16
+  void* h;               // [2][T*k, f] bf16: values, then what their rounding left
   float* y;              // [T*k, d]
   void* out;             // [T, d] bf16
   uint64_t wait_ns;      // limit of a wait

@@ -10,9 +10,9 @@
 //
 // Matrices with many strips are walked by blocks that stay (strip after strip,
 // the next one's weights in flight during the sums of the last).  Where strips
-// are fewer than twice the SMs, the inputs of a strip are split over a
-// cluster's blocks instead, which add their sums through each other's shared
-// memory: no scratch in memory, and no order that could change a result.
+// are no more than the SMs, the inputs of a strip are split over a cluster's
+// blocks instead, which add their sums through each other's shared memory: no
+// scratch in memory, and no order that could change a result.
 #include "int4.cuh"
 #include "int4_mma.cuh"
 #include "internal.h"
@@ -197,10 +197,12 @@ cudaError_t launch_linear_int4(const LinearInt4& p, int num_sms, cudaStream_t st
   a.strips = (p.N + kInt4Rows - 1) / kInt4Rows;
   if (a.p.row_strips > a.strips) a.p.row_strips = a.strips;
   a.units = (p.K + kInt4Unit - 1) / kInt4Unit;
-  // blocks for two an SM at most, and a stage of inputs for each at least
+  // Twice as many blocks while that is at most two an SM and half as many had
+  // more than a stage of inputs each.  So a block may get less than a stage, and
+  // the last ones none at all: they add zeros (17 units of inputs over 8
+  // blocks: 3 for each of five, 2 for one, none for two).
   a.split = 1;
   while (a.split < kMostSplit && a.strips * a.split * 2 <= 2 * num_sms && a.units > a.split * kStageUnits) a.split *= 2;
-  // (a last rank may be left without any: it adds zeros)
   a.units_per_rank = (a.units + a.split - 1) / a.split;
   a.stage_bytes = kStageUnits * int4_record_bytes(p.group);
   a.row_offset = kStages * a.stage_bytes;

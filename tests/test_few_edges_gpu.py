@@ -233,3 +233,36 @@ def test_matrix_beyond_32_bits():
         want = x.double() @ w
         size = x.double().abs() @ (8.0 * scales[:, part].double().repeat_interleave(128, 0))
         ref.check(out[:, part], want, ref.U * want.abs() + 7.0 * ref.gamma(K) * size)
+
+
+def test_fp8_range_of_scaled_inputs():
+    """x * scale and h * scale up to 2^67 in size are right; beyond, the token's output is not finite, and the others'
+    are untouched."""
+    d = f = 128
+    one = torch.zeros(1, d, f, dtype=torch.uint8, device="cuda")
+    one[:, 0] = 0x38  # 1.0 in E4M3, for the first input alone
+    coded = [(codes, torch.full((d,), scale, device="cuda")) for codes, scale in
+             ((one, 1.0), (one, 2.0 ** -70), (torch.full_like(one, 0x38), 2.0 ** -60))]
+    packed = moe.moe_pack_weights_fp8(*coded, 1, d, f)
+    x = torch.zeros(5, d, device="cuda")
+    x[:, 0] = torch.tensor([2.0 ** 40, 1.5 * 2.0 ** 66, 2.0 ** 69, 2.0 ** 66, 2.0 ** 50])
+    out = moe.moe_forward_few(x.to(torch.bfloat16), torch.zeros(5, 1, device="cuda"), packed, 1, 1, f, weights="fp8")
+    # silu(g) = g; every value is a power of two or 1.5 times one
+    want = (x[:, :1].double() ** 2 * 2.0 ** -70 * 2.0 ** -60 * f).expand(-1, d)
+    keep = [0, 1, 3, 4]
+    assert float(((out[keep].double() - want[keep]) / want[keep]).abs().max()) <= ref.U
+    assert not torch.isfinite(out[2]).any()
+
+
+def test_infinite_inputs_of_4_bit_experts():
+    """An infinite input makes its own token's output NaN, no other's."""
+    E, d, f, T = 3, 128, 128, 12
+    packed, mats = ref.weights("int4", E, d, f)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, d, generator=gen, device="cuda").to(torch.bfloat16)
+    x[5, 77] = math.inf
+    logits = torch.randn(T, E, generator=gen, device="cuda")
+    out = moe.moe_forward_few(x, logits, packed, E, 2, f, weights="int4")
+    keep = [t for t in range(T) if t != 5]
+    ref.check(out[keep], *ref.layer(x[keep], *ref.route(logits[keep], 2), mats, "int4"))
+    assert torch.isnan(out[5]).all()
