@@ -82,8 +82,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // of which it waits for.  (With one barrier for both groups, a ring of an odd
 // number of slots gives the groups a slot's fills in turn, and a group would
 // tell its next fill from its last by a parity that the other group's fill,
-// not yet there, leaves unchanged.)  So a barrier's phase is the number of
-// times round where the groups have slots of their own, and half of it where
+// not yet there, leaves unchanged.)  So the parity of a fill is that of the times
+// round where the groups have slots of their own, and of half of them where
 // they have them in turn.
 template <int kGroups>
 __device__ __forceinline__ uint32_t fill_phase(uint32_t wrap, int slots) {
