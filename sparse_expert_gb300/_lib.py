@@ -1150,12 +1150,14 @@ def _bytes_at_least(t, index, size, name):
     return t.data_ptr()
 
 
-def _packed_int4(t, index, size, group):
-    """A buffer of packed 4-bit weights.  It does not say what it was packed with, but its size does: another group
-    gives another size for the same matrices, and would be read as wrong weights.  (size 0: refused by the library.)"""
+def _packed_coded(t, index, size, weights, group):
+    """A buffer of packed FP8 or 4-bit weights.  It does not say what it was packed with, but its size does: another
+    format or group gives another size for the same matrices, and would be read as wrong weights.  (size 0: refused
+    by the library.)"""
     ptr = _bytes_at_least(t, index, size, "packed")
     if size and t.numel() != size:
-        raise ValueError(f"packed has {t.numel()} bytes, weights of these sizes packed with group={group} have {size}")
+        what = f"int4 (group={group})" if weights == "int4" else weights
+        raise ValueError(f"packed has {t.numel()} bytes, {what} weights of these sizes have {size}")
     return ptr
 
 
@@ -1171,7 +1173,10 @@ def _forward_few(entry, where, x, route, route_ptr, packed, E, k, f, weights, gr
     if kind is None:
         raise ValueError(f"weights must be one of {sorted(_WEIGHTS)}, got {weights!r}")
     size = _packed_bytes(weights, E, d, f, group)
-    p_ptr = _packed_int4(packed, index, size, group) if kind == 2 else _bytes_at_least(packed, index, size, "packed")
+    if kind:
+        p_ptr = _packed_coded(packed, index, size, weights, group)
+    else:  # no other format has as many bytes
+        p_ptr = _bytes_at_least(packed, index, size, "packed")
     dev = x.device
     if workspace is None:
         size = moe_forward_few_workspace_bytes(T, E, k, d, f)
@@ -1193,8 +1198,8 @@ def moe_forward_few(x, logits, packed, E, k, f, weights="bf16", group=128, renor
                     topk_idx=None, topk_w=None, stream=None):
     """out [T,d] of the whole layer for T <= 64 tokens, routed by logits [T,E].
     weights: "bf16" (packed by moe_pack_weights), "fp8" (moe_pack_weights_fp8) or
-    "int4" (moe_pack_weights_int4, with the same group: a buffer of another size
-    is refused); topk_idx, topk_w [T,k]: written where given."""
+    "int4" (moe_pack_weights_int4, with the same group); "fp8" and "int4" buffers
+    of another size are refused.  topk_idx, topk_w [T,k]: written where given."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_forward_few(x, logits, packed, E, k, f, weights, group, renormalize, workspace, out, topk_idx,
@@ -1306,7 +1311,7 @@ def moe_linear_int4(x, packed, N, group=128, out=None, stream=None):
         out, out_stride = torch.empty((M, N), dtype=torch.bfloat16, device=x.device), N
     else:
         out_stride = _rows(out, "out", index, (M, N), torch.bfloat16)
-    p_ptr = _packed_int4(packed, index, _linear_int4_bytes(K, N, group), group)
+    p_ptr = _packed_coded(packed, index, _linear_int4_bytes(K, N, group), "int4", group)
     status = lib.moe_linear_int4(x.data_ptr(), x_stride, p_ptr, M, K, N, group, out.data_ptr(), out_stride,
                                  _raw_stream(index))
     if status:
@@ -1333,7 +1338,7 @@ def moe_selftest_linear_int4_wait(x, packed, N, row_strips, limit_ns, group=128)
     x_stride = _rows(x, "x", index, None, torch.bfloat16)
     M, K = x.shape
     out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    p_ptr = _packed_int4(packed, index, _linear_int4_bytes(K, N, group), group)
+    p_ptr = _packed_coded(packed, index, _linear_int4_bytes(K, N, group), "int4", group)
     _check(lib.moe_selftest_linear_int4_wait(x.data_ptr(), x_stride, p_ptr, M, K, N, group, out.data_ptr(), N,
                                              int(row_strips), int(limit_ns), _raw_stream(index)),
            "moe_selftest_linear_int4_wait")

@@ -266,3 +266,17 @@ def test_infinite_inputs_of_4_bit_experts():
     keep = [t for t in range(T) if t != 5]
     ref.check(out[keep], *ref.layer(x[keep], *ref.route(logits[keep], 2), mats, "int4"))
     assert torch.isnan(out[5]).all()
+
+
+def test_weights_of_another_format_are_refused():
+    """bf16 weights take more bytes than the same in FP8 or 4 bits: too many are refused as too few are."""
+    E, d, f = 3, 128, 256
+    x, logits = bf16(2, d, value=1.0), torch.randn(2, E, device="cuda")
+    packed = {kind: ref.weights(kind, E, d, f)[0] for kind in KINDS}
+    for kind in KINDS:
+        for other in KINDS:
+            if kind == other:
+                moe.moe_forward_few(x, logits, packed[kind], E, 2, f, weights=kind)
+            else:
+                with pytest.raises(ValueError):
+                    moe.moe_forward_few(x, logits, packed[other], E, 2, f, weights=kind)
